@@ -51,6 +51,20 @@ typedef void* pkv_stream_t; /* a cudaStream_t */
  * infinities); queries and outputs are F32, F16 or BF16. */
 typedef enum { PKV_F32 = 0, PKV_F16 = 1, PKV_BF16 = 2, PKV_FP8_E4M3 = 3 } pkv_dtype;
 
+/* Pools of 8-bit rows ("int8 pools"), a further pool type, used by the calls
+ * named *_int8 (and as the dtype of pkv_decode_partition_size).  A row is one
+ * token's head_dim elements of one KV head, stored as one-byte codes
+ *     u = 128 + rint(x / s)    (fp32 quotient, ties to even)
+ * with a scale of its own, s = max |x| / 127 in fp32, and stands for
+ * s * (u - 128).  No calibration is needed: every row uses its full range.
+ * The bytes of a block are the codes [block_size, num_kv_heads, head_dim] and
+ * then the scales, float [num_kv_heads, block_size]:
+ * pkv_int8_block_bytes(...) = block_size * num_kv_heads * (head_dim + 4) in
+ * all, so pkv_copy_blocks and pkv_swap_blocks move whole blocks with that
+ * block_bytes.  s is at least 2^-80 (a zero row has codes 128); a row that
+ * holds a NaN or an infinity gets the scale NaN and reads as NaN. */
+#define PKV_INT8 4
+
 typedef enum {
     PKV_OK = 0,
     PKV_EINVAL = -1,         /* null pointer, negative size, misaligned pointer */
@@ -66,6 +80,7 @@ typedef enum {
 #define PKV_DEVERR_LENGTH     0x4u  /* context / sequence length beyond the table, or a bad chunk */
 #define PKV_DEVERR_PAIR       0x8u  /* copy_blocks pair outside [0, num_blocks) */
 #define PKV_DEVERR_TIMEOUT    0x10u /* a bounded wait on an asynchronous copy or MMA gave up */
+#define PKV_DEVERR_POSITION   0x20u /* a position outside the rotary table */
 
 /* Human-readable name of a pkv_status. */
 const char* pkv_status_string(int status);
@@ -118,6 +133,118 @@ int pkv_reshape_and_cache_fp8(const void* key, const void* value, void* key_cach
                               const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads, int head_dim,
                               int block_size, int64_t num_blocks, int src_dtype, float k_scale, float v_scale,
                               pkv_stream_t stream);
+
+/*
+ * Rotary positions.  Row p of a rotary table holds, for the R = rotary_dim
+ * rotated elements of a head and i < R / 2,
+ *     cos_sin[p][i] = a cos(p theta_i),   cos_sin[p][R/2 + i] = a sin(p theta_i)
+ * with a = attention_factor and frequencies theta_i = base^(-2 i / R), changed
+ * for contexts longer than the model was trained on by `scaling`:
+ *   PKV_ROPE_NONE      as they are
+ *   PKV_ROPE_LINEAR    theta_i / factor (position interpolation)
+ *   PKV_ROPE_NTK       the base becomes base * factor^(R / (R - 2))
+ *   PKV_ROPE_BY_PARTS  with r_i = original_max_position * theta_i / (2 pi) turns
+ *                      over the trained context and g = clamp((r_i - alpha) /
+ *                      (beta - alpha), 0, 1):  (1 - g) theta_i / factor + g theta_i
+ * ("YaRN: Efficient Context Window Extension of Large Language Models", Peng
+ * et al. 2023, section 3, states the last three.)  Fields a scaling does not
+ * use are ignored.
+ */
+typedef enum { PKV_ROPE_NONE = 0, PKV_ROPE_LINEAR = 1, PKV_ROPE_NTK = 2, PKV_ROPE_BY_PARTS = 3 } pkv_rope_scaling;
+
+typedef struct {
+    double base;                    /* > 0, e.g. 10000 */
+    double factor;                  /* > 0 */
+    double alpha, beta;             /* alpha < beta */
+    double attention_factor;        /* finite */
+    int64_t original_max_position;  /* > 0 */
+    int32_t rotary_dim;             /* R: a multiple of 8, 8 to 256 (16 at least for NTK) */
+    int32_t scaling;                /* a pkv_rope_scaling */
+} pkv_rope_spec;
+
+/* Rows [first_position, first_position + num_positions) of the table into
+ * cos_sin (device float [num_positions, rotary_dim]); `spec` is host memory.
+ * Angles are formed in 64 bits; first_position + num_positions <= 2^40. */
+int pkv_rope_table(float* cos_sin, int64_t first_position, int64_t num_positions, const pkv_rope_spec* spec,
+                   pkv_stream_t stream);
+
+/*
+ * What lies between a layer's projections and its attention, in one pass: the
+ * norm of every query and key head, rotary positions, and the append.
+ * For token t with position p = positions[t], and every query and key head x
+ * of head_dim elements:
+ *   1. with a norm weight w (one for queries, one for keys, each may be NULL:
+ *      no norm):  x_d <- x_d / sqrt(mean_d x_d^2 + eps) * w_d
+ *   2. the first R = rotary_dim elements rotate in pairs by row p of cos_sin:
+ *      (x_a, x_b) <- (x_a c_i - x_b s_i, x_a s_i + x_b c_i),  pair i being
+ *      (i, i + R/2), or (2 i, 2 i + 1) with `interleaved` != 0; the others stay.
+ * Queries go to query_out; keys, and values as they are, go to slot
+ * slot_mapping[t] of the pools as pkv_reshape_and_cache (or _fp8, _int8)
+ * writes them.  Everything is computed in fp32 and rounded once, to the
+ * output's or pool's type.
+ *
+ *   query, key, value   device, dtype; token t's heads start at element
+ *                   t * {query,key,value}_stride and are contiguous, so the
+ *                   three may be slices of one projection's output
+ *   query_out       device [num_tokens, num_q_heads, head_dim], dtype; may be
+ *                   `query` itself when query_stride == num_q_heads * head_dim
+ *   q_norm_weight, k_norm_weight   device [head_dim], dtype, or NULL
+ *   cos_sin         device float [max_position, rotary_dim] (pkv_rope_table)
+ *   positions       device int64 [num_tokens]; a token whose position is
+ *                   outside [0, max_position) is skipped (no query row, no
+ *                   append) and sets PKV_DEVERR_POSITION
+ *   slot_mapping    as for pkv_reshape_and_cache; a token with a negative slot
+ *                   still gets its query row
+ * Supported: dtype in {F32, F16, BF16}; head_dim a multiple of 8, at most 256
+ * (16 for E4M3 and int8 pools); rotary_dim a multiple of 8, 0 <= R <= head_dim
+ * (0: no rotation; cos_sin may be NULL and positions are then not read and may
+ * be NULL).  Strides are multiples of 16 bytes.  num_tokens == 0 is a no-op.
+ */
+int pkv_rope_and_cache(void* query_out, const void* query, const void* key, const void* value, int64_t query_stride,
+                       int64_t key_stride, int64_t value_stride, const void* q_norm_weight, const void* k_norm_weight,
+                       float eps, const float* cos_sin, int64_t max_position, int rotary_dim, int interleaved,
+                       const int64_t* positions, void* key_cache, void* value_cache, const int64_t* slot_mapping,
+                       int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                       int64_t num_blocks, int dtype, pkv_stream_t stream);
+
+/* The same into E4M3 pools (one scale per pool). */
+int pkv_rope_and_cache_fp8(void* query_out, const void* query, const void* key, const void* value,
+                           int64_t query_stride, int64_t key_stride, int64_t value_stride, const void* q_norm_weight,
+                           const void* k_norm_weight, float eps, const float* cos_sin, int64_t max_position,
+                           int rotary_dim, int interleaved, const int64_t* positions, void* key_cache,
+                           void* value_cache, const int64_t* slot_mapping, int64_t num_tokens, int num_q_heads,
+                           int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, int dtype,
+                           float k_scale, float v_scale, pkv_stream_t stream);
+
+/* The same into int8 pools: a key row's scale is taken after its rotation. */
+int pkv_rope_and_cache_int8(void* query_out, const void* query, const void* key, const void* value,
+                            int64_t query_stride, int64_t key_stride, int64_t value_stride, const void* q_norm_weight,
+                            const void* k_norm_weight, float eps, const float* cos_sin, int64_t max_position,
+                            int rotary_dim, int interleaved, const int64_t* positions, void* key_cache,
+                            void* value_cache, const int64_t* slot_mapping, int64_t num_tokens, int num_q_heads,
+                            int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, int dtype,
+                            pkv_stream_t stream);
+
+/* Bytes of one block of an int8 pool: block_size * num_kv_heads * (head_dim +
+ * 4); PKV_EINVAL for sizes <= 0. */
+int64_t pkv_int8_block_bytes(int block_size, int num_kv_heads, int head_dim);
+
+/* Write new tokens' K and V rows into int8 pools, quantising on the way.
+ * Arguments as for pkv_reshape_and_cache_fp8 without the scales; the pools are
+ * num_blocks blocks of pkv_int8_block_bytes.  head_dim: a multiple of 16, at
+ * most 256; block_size * num_kv_heads a multiple of 4. */
+int pkv_reshape_and_cache_int8(const void* key, const void* value, void* key_cache, void* value_cache,
+                               const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads, int head_dim,
+                               int block_size, int64_t num_blocks, int src_dtype, pkv_stream_t stream);
+
+/* The rows of the listed slots read back as values, s * (u - 128) rounded once
+ * to dst_dtype (F32, F16 or BF16):
+ *   key_out, value_out   device [num_tokens, num_kv_heads, head_dim]
+ * A negative slot's rows are left as they were (so are those of a slot beyond
+ * the pool, which sets PKV_DEVERR_SLOT).  A slot may be listed more than once. */
+int pkv_read_cache_int8(void* key_out, void* value_out, const void* key_cache, const void* value_cache,
+                        const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads, int head_dim,
+                        int block_size, int64_t num_blocks, int dst_dtype, pkv_stream_t stream);
 
 /*
  * copy_blocks -- copy-on-write of shared blocks.  Source: case-study page

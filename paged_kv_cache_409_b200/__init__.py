@@ -8,6 +8,7 @@ load the library; the first call does, and fails loudly if it is missing.
 from ._binding import (  # noqa: F401
     FP8_E4M3,
     FP8_POOL_DTYPES,
+    INT8,
     PagedKVError,
     copy_blocks,
     decode_multi_partition_size,
@@ -15,6 +16,8 @@ from ._binding import (  # noqa: F401
     decode_workspace_size,
     prefill_fp8_workspace_size,
     get_device_error,
+    int8_block_bytes,
+    int8_pool_views,
     library_path,
     load_library,
     paged_attention_decode,
@@ -25,8 +28,14 @@ from ._binding import (  # noqa: F401
     paged_attention_decode_multi_step,
     paged_attention_prefill_chunk,
     paged_attention_prefill_chunk_fp8,
+    read_cache_int8,
     reshape_and_cache,
     reshape_and_cache_fp8,
+    reshape_and_cache_int8,
+    rope_and_cache,
+    rope_and_cache_fp8,
+    rope_and_cache_int8,
+    rope_table,
     set_wait_limit_ns,
     DEFAULT_WAIT_LIMIT_NS,
     swap_blocks,

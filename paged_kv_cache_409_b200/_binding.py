@@ -20,12 +20,16 @@ _lib = None
 DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 FP8_E4M3 = 3
 FP8_POOL_DTYPES = (torch.uint8, torch.float8_e4m3fn)  # one E4M3 code per element
+INT8 = 4  # pools of 8-bit rows, a scale for each row
 
 DEVERR_BLOCK_ID = 0x1
 DEVERR_SLOT = 0x2
 DEVERR_LENGTH = 0x4
 DEVERR_PAIR = 0x8
 DEVERR_TIMEOUT = 0x10
+DEVERR_POSITION = 0x20
+
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 EXPORTED = (
     "pkv_status_string",
@@ -49,7 +53,21 @@ EXPORTED = (
     "pkv_decode_multi_partition_size",
     "pkv_get_device_error",
     "pkv_set_wait_limit_ns",
+    "pkv_rope_table",
+    "pkv_rope_and_cache",
+    "pkv_rope_and_cache_fp8",
+    "pkv_rope_and_cache_int8",
+    "pkv_int8_block_bytes",
+    "pkv_reshape_and_cache_int8",
+    "pkv_read_cache_int8",
 )
+
+
+class RopeSpec(ctypes.Structure):
+    """``pkv_rope_spec``."""
+    _fields_ = [("base", ctypes.c_double), ("factor", ctypes.c_double), ("alpha", ctypes.c_double),
+                ("beta", ctypes.c_double), ("attention_factor", ctypes.c_double),
+                ("original_max_position", ctypes.c_int64), ("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32)]
 
 
 class PagedKVError(RuntimeError):
@@ -104,13 +122,24 @@ def load_library():
     lib.pkv_paged_attention_decode_step_fp8.argtypes = [P, P, P, I64, P, P, P, P, P, P, F, F, F, I, I, I, I, I, I,
                                                         I64, I, I, I, P, SZ, P]
     lib.pkv_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
+    lib.pkv_rope_table.argtypes = [P, I64, I64, ctypes.POINTER(RopeSpec), P]
+    rope = [P, P, P, P, I64, I64, I64, P, P, F, P, I64, I, I, P, P, P, P, I64, I, I, I, I, I64, I]
+    lib.pkv_rope_and_cache.argtypes = rope + [P]
+    lib.pkv_rope_and_cache_fp8.argtypes = rope + [F, F, P]
+    lib.pkv_rope_and_cache_int8.argtypes = rope + [P]
+    lib.pkv_int8_block_bytes.argtypes = [I, I, I]
+    lib.pkv_int8_block_bytes.restype = I64
+    lib.pkv_reshape_and_cache_int8.argtypes = [P, P, P, P, P, I64, I, I, I, I64, I, P]
+    lib.pkv_read_cache_int8.argtypes = [P, P, P, P, P, I64, I, I, I, I64, I, P]
     for name in ("pkv_reshape_and_cache", "pkv_reshape_and_cache_fp8", "pkv_paged_attention_decode_fp8",
                  "pkv_copy_blocks", "pkv_swap_blocks", "pkv_paged_attention_decode",
                  "pkv_decode_partition_size", "pkv_paged_attention_prefill_chunk", "pkv_get_device_error",
                  "pkv_paged_attention_prefill_chunk_fp8", "pkv_paged_attention_decode_multi",
                  "pkv_paged_attention_decode_multi_step",
                  "pkv_decode_multi_partition_size", "pkv_paged_attention_decode_step",
-                 "pkv_paged_attention_decode_step_fp8", "pkv_set_wait_limit_ns"):
+                 "pkv_paged_attention_decode_step_fp8", "pkv_set_wait_limit_ns", "pkv_rope_table",
+                 "pkv_rope_and_cache", "pkv_rope_and_cache_fp8", "pkv_rope_and_cache_int8",
+                 "pkv_reshape_and_cache_int8", "pkv_read_cache_int8"):
         getattr(lib, name).restype = I
     _lib = lib
     return lib
@@ -130,6 +159,13 @@ def _dev(t: torch.Tensor, name: str) -> int:
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _here(t: torch.Tensor, name: str) -> int:
+    """As :func:`_dev`, for a tensor that must live on the current device."""
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return _dev(t, name)
 
 
 def _code(t: torch.Tensor) -> int:
@@ -484,6 +520,161 @@ def paged_attention_decode_multi_step(new_keys, new_values, slot_mapping, out, q
         B, MB, NB, int(partition_size), _code(query), ws_ptr, ws_bytes, _stream(stream))
     _ok(rc, "paged_attention_decode_multi_step")
     return out
+
+
+# ---------------------------------------------------------------- rotary positions, and pools of 8-bit rows
+def rope_table(cos_sin, base=10000.0, first_position=0, scaling="none", factor=1.0, alpha=1.0, beta=32.0,
+               original_max_position=1, attention_factor=1.0, stream=None):
+    """Fill ``cos_sin`` (fp32 ``[positions, rotary_dim]``) with the rotary table's rows from ``first_position`` on:
+    the cosines, then the sines, of ``position * theta_i``, times ``attention_factor``.  ``scaling``: "none",
+    "linear", "ntk" or "by_parts" (see ``pkv_rope_table``)."""
+    lib = load_library()
+    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
+        raise ValueError("cos_sin must be a float32 [positions, rotary_dim] tensor")
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}")
+    spec = RopeSpec(float(base), float(factor), float(alpha), float(beta), float(attention_factor),
+                    int(original_max_position), cos_sin.shape[1], ROPE_SCALING[scaling])
+    rc = lib.pkv_rope_table(_here(cos_sin, "cos_sin"), int(first_position), cos_sin.shape[0], ctypes.byref(spec),
+                            _stream(stream))
+    _ok(rc, "rope_table")
+    return cos_sin
+
+
+def _head_rows(t: torch.Tensor, name: str):
+    """(pointer, elements between tokens) of ``[T, H, D]`` rows whose heads are contiguous within a token, as in a
+    slice of a projection's output."""
+    T, H, D = t.shape
+    if t.stride(2) != 1 and D > 1 or t.stride(1) != D and H > 1:
+        raise ValueError(f"{name}'s heads must be contiguous within a token")
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return _dev(t[:1].reshape(-1), name) if T else t.data_ptr(), t.stride(0) if T > 1 else H * D
+
+
+def _rope_and_cache(name, query_out, query, key, value, cos_sin, positions, pools, pool_shape, slot_mapping, interleaved,
+                    q_norm_weight, k_norm_weight, eps, scales, stream):
+    lib = load_library()
+    T, Hq, D = query.shape
+    NB, B, Hkv, Dp = pool_shape
+    if key.shape != (T, Hkv, D) or value.shape != (T, Hkv, D) or Dp != D:
+        raise ValueError("key and value must be [tokens, num_kv_heads, head_dim] of the query's tokens and the pools")
+    if query_out.shape != query.shape or not query_out.dtype == query.dtype == key.dtype == value.dtype:
+        raise ValueError("query_out, query, key and value must agree in dtype, query_out and query in shape")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be int64 [tokens]")
+    rotary_dim = max_position = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
+            raise ValueError("cos_sin must be a float32 [positions, rotary_dim] tensor")
+        if positions is None or positions.dtype != torch.int64 or positions.shape != (T,):
+            raise ValueError("positions must be int64 [tokens]")
+        max_position, rotary_dim = cos_sin.shape
+    for w, what in ((q_norm_weight, "q_norm_weight"), (k_norm_weight, "k_norm_weight")):
+        if w is not None and (w.dtype != query.dtype or w.shape != (D,)):
+            raise ValueError(f"{what} must be [head_dim] in the query's dtype")
+    q, qs = _head_rows(query, "query")
+    k, ks = _head_rows(key, "key")
+    v, vs = _head_rows(value, "value")
+    opt = lambda t, what: None if t is None else _here(t, what)  # noqa: E731
+    rc = getattr(lib, "pkv_" + name)(
+        _here(query_out, "query_out"), q, k, v, qs, ks, vs, opt(q_norm_weight, "q_norm_weight"),
+        opt(k_norm_weight, "k_norm_weight"), float(eps), opt(cos_sin, "cos_sin"), max_position, rotary_dim,
+        int(bool(interleaved)), opt(positions if rotary_dim else None, "positions"), pools[0], pools[1],
+        _here(slot_mapping, "slot_mapping"), T, Hq, Hkv, D, B, NB, _code(query), *scales, _stream(stream))
+    _ok(rc, name)
+    return query_out
+
+
+def rope_and_cache(query_out, query, key, value, cos_sin, positions, key_cache, value_cache, slot_mapping,
+                   interleaved=False, q_norm_weight=None, k_norm_weight=None, eps=1e-6, stream=None):
+    """Norm of every query and key head (weights ``[D]``, or None), rotary positions (rows ``positions`` of
+    ``cos_sin``, or None) and the append, in one pass: queries ``[T, Hq, D]`` to ``query_out``, keys and values
+    ``[T, Hkv, D]`` to the pools' slots.  Query, key and value may be slices of one projection's output."""
+    if key_cache.dtype != query.dtype or value_cache.dtype != query.dtype or key_cache.shape != value_cache.shape:
+        raise ValueError("the pools must have the query's dtype and one shape")
+    return _rope_and_cache("rope_and_cache", query_out, query, key, value, cos_sin, positions,
+                           (_here(key_cache, "key_cache"), _here(value_cache, "value_cache")), key_cache.shape,
+                           slot_mapping, interleaved, q_norm_weight, k_norm_weight, eps, (), stream)
+
+
+def rope_and_cache_fp8(query_out, query, key, value, cos_sin, positions, key_cache, value_cache, slot_mapping, k_scale,
+                       v_scale, interleaved=False, q_norm_weight=None, k_norm_weight=None, eps=1e-6, stream=None):
+    """:func:`rope_and_cache` into E4M3 pools."""
+    if key_cache.shape != value_cache.shape:
+        raise ValueError("the pools must have one shape")
+    return _rope_and_cache("rope_and_cache_fp8", query_out, query, key, value, cos_sin, positions,
+                           (_fp8_pool(key_cache, "key_cache"), _fp8_pool(value_cache, "value_cache")), key_cache.shape,
+                           slot_mapping, interleaved, q_norm_weight, k_norm_weight, eps,
+                           (float(k_scale), float(v_scale)), stream)
+
+
+def rope_and_cache_int8(query_out, query, key, value, cos_sin, positions, key_cache, value_cache, slot_mapping,
+                        interleaved=False, q_norm_weight=None, k_norm_weight=None, eps=1e-6, stream=None):
+    """:func:`rope_and_cache` into int8 pools."""
+    shape, k, v = _int8_pools(key_cache, value_cache)
+    return _rope_and_cache("rope_and_cache_int8", query_out, query, key, value, cos_sin, positions, (k, v), shape,
+                           slot_mapping, interleaved, q_norm_weight, k_norm_weight, eps, (), stream)
+
+
+def int8_block_bytes(block_size, num_kv_heads, head_dim) -> int:
+    """Bytes of one block of an int8 pool, ``block_size * num_kv_heads * (head_dim + 4)``."""
+    rc = int(load_library().pkv_int8_block_bytes(block_size, num_kv_heads, head_dim))
+    if rc < 0:
+        raise PagedKVError("int8_block_bytes", rc)
+    return rc
+
+
+def int8_pool_views(pool):
+    """``(codes, scales)`` of an int8 pool, uint8 ``[NB, B, Hkv, D + 4]``, as views of it: the codes uint8
+    ``[NB, B, Hkv, D]`` (zero point 128) and the scales float32 ``[NB, Hkv, B]``."""
+    NB, B, H, W = pool.shape
+    flat = pool.view(NB, B * H * W)
+    n = B * H * (W - 4)
+    return flat[:, :n].view(NB, B, H, W - 4), flat.view(torch.float32)[:, n // 4:].view(NB, H, B)
+
+
+def _int8_pools(key_cache, value_cache):
+    """((NB, B, Hkv, D), key pointer, value pointer) of two int8 pools."""
+    for t, name in ((key_cache, "key_cache"), (value_cache, "value_cache")):
+        if t.dtype != torch.uint8 or t.dim() != 4 or t.shape[3] <= 4:
+            raise ValueError(f"{name} must be a uint8 [blocks, block_size, num_kv_heads, head_dim + 4] pool")
+    if key_cache.shape != value_cache.shape:
+        raise ValueError("key_cache and value_cache differ in shape")
+    NB, B, H, W = key_cache.shape
+    return (NB, B, H, W - 4), _here(key_cache, "key_cache"), _here(value_cache, "value_cache")
+
+
+def reshape_and_cache_int8(key, value, key_cache, value_cache, slot_mapping, stream=None):
+    """Quantise ``key``/``value`` ``[T, Hkv, D]`` (fp32/fp16/bf16) row by row into the int8 pools' slots
+    ``slot_mapping`` (int64, -1 = skip)."""
+    lib = load_library()
+    (NB, B, H, D), k, v = _int8_pools(key_cache, value_cache)
+    T = slot_mapping.numel()
+    if slot_mapping.dtype != torch.int64:
+        raise ValueError("slot_mapping must be int64")
+    if key.shape != (T, H, D) or value.shape != (T, H, D) or key.dtype != value.dtype:
+        raise ValueError("key and value must be [tokens, num_kv_heads, head_dim] of the pools, in one dtype")
+    rc = lib.pkv_reshape_and_cache_int8(_here(key, "key"), _here(value, "value"), k, v,
+                                        _here(slot_mapping, "slot_mapping"), T, H, D, B, NB, _code(key),
+                                        _stream(stream))
+    _ok(rc, "reshape_and_cache_int8")
+
+
+def read_cache_int8(key_out, value_out, key_cache, value_cache, slot_mapping, stream=None):
+    """The rows of ``slot_mapping``'s slots of two int8 pools as values, into ``key_out``/``value_out``
+    ``[T, Hkv, D]`` (fp32/fp16/bf16); the rows of negative slots are left as they were."""
+    lib = load_library()
+    (NB, B, H, D), k, v = _int8_pools(key_cache, value_cache)
+    T = slot_mapping.numel()
+    if slot_mapping.dtype != torch.int64:
+        raise ValueError("slot_mapping must be int64")
+    if key_out.shape != (T, H, D) or value_out.shape != (T, H, D) or key_out.dtype != value_out.dtype:
+        raise ValueError("key_out and value_out must be [tokens, num_kv_heads, head_dim] of the pools, in one dtype")
+    rc = lib.pkv_read_cache_int8(_here(key_out, "key_out"), _here(value_out, "value_out"), k, v,
+                                 _here(slot_mapping, "slot_mapping"), T, H, D, B, NB, _code(key_out), _stream(stream))
+    _ok(rc, "read_cache_int8")
+    return key_out, value_out
 
 
 def get_device_error(stream=None) -> int:

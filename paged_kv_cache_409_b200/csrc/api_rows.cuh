@@ -1,0 +1,273 @@
+// api_rows.cuh -- host side of the row calls (row_kernels.cuh): rotary tables,
+// norm + rotation + append, and the append and read of 8-bit rows.  Included
+// at the end of pagedkv.cu (one translation unit, one error word).
+
+namespace {
+
+// Lanes per row of head_dim elements, eight elements each.
+int row_lanes(int head_dim) { return head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32; }
+
+// The shape rules of int8 pools: 16-byte rows of codes and 16-byte blocks.
+bool int8_shape(int num_kv_heads, int head_dim, int block_size) {
+    return head_dim % 16 == 0 && head_dim <= 256 && (int64_t)block_size * num_kv_heads % 4 == 0 &&
+           (int64_t)block_size * num_kv_heads * (head_dim + 4) <= INT32_MAX;
+}
+
+int check_slots(const int64_t* slot_mapping, int64_t num_tokens, int64_t num_slots, cudaStream_t s) {
+    if (!checked_mode()) return PKV_OK;
+    std::vector<int64_t> sm;
+    int rc = fetch(sm, slot_mapping, (size_t)num_tokens, s);
+    if (rc) return rc;
+    for (int64_t v : sm)
+        if (v >= num_slots) return PKV_ERANGE;
+    return PKV_OK;
+}
+
+// Argument checks of the append into and the read from int8 pools (x, y: the
+// rows outside the pools).
+int rows_int8_check(const void* x, const void* y, const void* key_cache, const void* value_cache,
+                    const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads, int head_dim, int block_size,
+                    int64_t num_blocks, int dtype) {
+    if (!query_type(dtype)) return PKV_EUNSUPPORTED;
+    if (num_tokens < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0) return PKV_EINVAL;
+    if (!int8_shape(num_kv_heads, head_dim, block_size)) return PKV_EUNSUPPORTED;
+    if (num_tokens == 0) return PKV_OK;
+    if (!x || !y || !key_cache || !value_cache || !slot_mapping) return PKV_EINVAL;
+    if (!aligned16(x) || !aligned16(y) || !aligned16(key_cache) || !aligned16(value_cache) ||
+        (reinterpret_cast<uintptr_t>(slot_mapping) & 7))
+        return PKV_EINVAL;
+    return PKV_OK;
+}
+
+template <typename TS>
+int launch_append_int8(const void* key, const void* value, void* kc, void* vc, const int64_t* slots, int64_t tokens,
+                       int heads, int dim, int block_size, int64_t num_slots, cudaStream_t s) {
+    const int lanes = row_lanes(dim);
+    const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(tokens * 2 * heads, 128 / lanes), 1 << 20);
+    auto kern = lanes == 8    ? pkv::append_int8_kernel<TS, 8>
+                : lanes == 16 ? pkv::append_int8_kernel<TS, 16>
+                              : pkv::append_int8_kernel<TS, 32>;
+    kern<<<grid, 128, 0, s>>>(static_cast<const TS*>(key), static_cast<const TS*>(value), static_cast<uint8_t*>(kc),
+                              static_cast<uint8_t*>(vc), slots, tokens, heads, dim, block_size, num_slots);
+    PKV_CUDA(cudaGetLastError());
+    return PKV_OK;
+}
+
+template <typename TD>
+int launch_read_int8(void* key, void* value, const void* kc, const void* vc, const int64_t* slots, int64_t tokens,
+                     int heads, int dim, int block_size, int64_t num_slots, cudaStream_t s) {
+    const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(tokens * 2 * heads * (dim / 8), 128), 1 << 20);
+    pkv::read_int8_kernel<TD><<<grid, 128, 0, s>>>(static_cast<TD*>(key), static_cast<TD*>(value),
+                                                   static_cast<const uint8_t*>(kc), static_cast<const uint8_t*>(vc),
+                                                   slots, tokens, heads, dim, block_size, num_slots);
+    PKV_CUDA(cudaGetLastError());
+    return PKV_OK;
+}
+
+template <typename T, int kPool>
+int launch_rope(const pkv::RopeRowsParams& p, cudaStream_t s) {
+    const int lanes = row_lanes(p.head_dim);
+    const int rows = p.num_q_heads + 2 * p.num_kv_heads;
+    const dim3 grid((unsigned)p.num_tokens, (unsigned)std::min<int64_t>(ceil_div(rows, 128 / lanes), 65535));
+    auto kern = lanes == 8    ? pkv::rope_rows_kernel<T, kPool, 8>
+                : lanes == 16 ? pkv::rope_rows_kernel<T, kPool, 16>
+                              : pkv::rope_rows_kernel<T, kPool, 32>;
+    kern<<<grid, 128, 0, s>>>(p);
+    PKV_CUDA(cudaGetLastError());
+    return PKV_OK;
+}
+
+template <int kPool>
+int rope_impl(void* query_out, const void* query, const void* key, const void* value, int64_t query_stride,
+              int64_t key_stride, int64_t value_stride, const void* q_norm_weight, const void* k_norm_weight, float eps,
+              const float* cos_sin, int64_t max_position, int rotary_dim, int interleaved, const int64_t* positions,
+              void* key_cache, void* value_cache, const int64_t* slot_mapping, int64_t num_tokens, int num_q_heads,
+              int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, int dtype, float k_scale,
+              float v_scale, pkv_stream_t stream) {
+    if (!query_type(dtype)) return PKV_EUNSUPPORTED;
+    if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
+        num_blocks <= 0 || rotary_dim < 0 || rotary_dim > head_dim || max_position < 0 || !(eps >= 0.f) ||
+        !std::isfinite(eps))
+        return PKV_EINVAL;
+    if (kPool == pkv::kPoolE4M3 &&
+        !(std::isfinite(k_scale) && k_scale > 0.f && std::isfinite(v_scale) && v_scale > 0.f))
+        return PKV_EINVAL;
+    if (head_dim % 8 || head_dim > 256 || rotary_dim % 8) return PKV_EUNSUPPORTED;
+    if (kPool == pkv::kPoolE4M3 && head_dim % 16) return PKV_EUNSUPPORTED;
+    if (kPool == pkv::kPoolInt8 && !int8_shape(num_kv_heads, head_dim, block_size)) return PKV_EUNSUPPORTED;
+    if (num_tokens == 0) return PKV_OK;
+    if (num_tokens > INT32_MAX || (int64_t)num_q_heads + 2 * (int64_t)num_kv_heads > INT32_MAX / 256)
+        return PKV_EUNSUPPORTED;
+    if (!query_out || !query || !key || !value || !key_cache || !value_cache || !slot_mapping) return PKV_EINVAL;
+    if (rotary_dim > 0 && (!cos_sin || !positions)) return PKV_EINVAL;
+    const int eb = elem_bytes(dtype);
+    const int64_t qrow = (int64_t)num_q_heads * head_dim, krow = (int64_t)num_kv_heads * head_dim;
+    if (query_stride < qrow || key_stride < krow || value_stride < krow) return PKV_EINVAL;
+    if (query_out == query && query_stride != qrow) return PKV_EINVAL;
+    const void* ptrs[9] = {query_out, query, key, value, key_cache, value_cache, q_norm_weight, k_norm_weight, cos_sin};
+    for (const void* q : ptrs)
+        if (!aligned16(q)) return PKV_EINVAL;
+    if (query_stride * eb % 16 || key_stride * eb % 16 || value_stride * eb % 16 ||
+        (reinterpret_cast<uintptr_t>(positions) & 7) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7))
+        return PKV_EINVAL;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t num_slots = num_blocks * block_size;
+    if (checked_mode()) {
+        int rc = check_slots(slot_mapping, num_tokens, num_slots, s);
+        if (rc) return rc;
+        if (rotary_dim > 0) {
+            std::vector<int64_t> ps;
+            rc = fetch(ps, positions, (size_t)num_tokens, s);
+            if (rc) return rc;
+            for (int64_t v : ps)
+                if (v < 0 || v >= max_position) return PKV_ERANGE;
+        }
+    }
+    pkv::RopeRowsParams p;
+    p.query_out = query_out;
+    p.query = query, p.key = key, p.value = value;
+    p.q_stride = query_stride, p.k_stride = key_stride, p.v_stride = value_stride;
+    p.q_weight = q_norm_weight, p.k_weight = k_norm_weight;
+    p.eps = eps;
+    p.cos_sin = cos_sin;
+    p.max_position = max_position;
+    p.rotary_dim = rotary_dim;
+    p.interleaved = interleaved != 0;
+    p.positions = rotary_dim > 0 ? positions : nullptr;
+    p.key_cache = key_cache, p.value_cache = value_cache;
+    p.slot_mapping = slot_mapping;
+    p.num_tokens = num_tokens, p.num_slots = num_slots;
+    p.num_q_heads = num_q_heads, p.num_kv_heads = num_kv_heads, p.head_dim = head_dim, p.block_size = block_size;
+    p.k_scale = k_scale, p.v_scale = v_scale;
+    switch (dtype) {
+        case PKV_F32: return launch_rope<float, kPool>(p, s);
+        case PKV_F16: return launch_rope<__half, kPool>(p, s);
+        default: return launch_rope<__nv_bfloat16, kPool>(p, s);
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkv_rope_table(float* cos_sin, int64_t first_position, int64_t num_positions, const pkv_rope_spec* spec,
+                   pkv_stream_t stream) {
+    if (!spec) return PKV_EINVAL;
+    const int R = spec->rotary_dim;
+    if (spec->scaling < PKV_ROPE_NONE || spec->scaling > PKV_ROPE_BY_PARTS) return PKV_EUNSUPPORTED;
+    if (R <= 0 || first_position < 0 || num_positions < 0 || !(spec->base > 0) || !std::isfinite(spec->base) ||
+        !std::isfinite(spec->attention_factor))
+        return PKV_EINVAL;
+    constexpr int64_t kFar = int64_t(1) << 40;
+    if (first_position > kFar || num_positions > kFar - first_position) return PKV_EINVAL;
+    if (spec->scaling != PKV_ROPE_NONE && !(spec->factor > 0 && std::isfinite(spec->factor))) return PKV_EINVAL;
+    if (spec->scaling == PKV_ROPE_BY_PARTS &&
+        !(spec->original_max_position > 0 && std::isfinite(spec->alpha) && std::isfinite(spec->beta) &&
+          spec->alpha < spec->beta))
+        return PKV_EINVAL;
+    if (R % 8 || R > 256 || (spec->scaling == PKV_ROPE_NTK && R < 16)) return PKV_EUNSUPPORTED;
+    if (num_positions == 0) return PKV_OK;
+    if (!cos_sin || !aligned16(cos_sin)) return PKV_EINVAL;
+    const double pi = 3.14159265358979323846;
+    pkv::RopeTableParams p;
+    p.out = cos_sin;
+    p.first = first_position;
+    p.count = num_positions;
+    p.half = R / 2;
+    p.attention_factor = spec->attention_factor;
+    const double base =
+        spec->scaling == PKV_ROPE_NTK ? spec->base * std::pow(spec->factor, (double)R / (R - 2)) : spec->base;
+    for (int i = 0; i < R / 2; ++i) {
+        double theta = std::pow(base, -2.0 * i / R);
+        if (spec->scaling == PKV_ROPE_LINEAR) theta /= spec->factor;
+        if (spec->scaling == PKV_ROPE_BY_PARTS) {
+            const double turns = spec->original_max_position * theta / (2 * pi);
+            const double g = std::min(1.0, std::max(0.0, (turns - spec->alpha) / (spec->beta - spec->alpha)));
+            theta = (1 - g) * theta / spec->factor + g * theta;
+        }
+        p.turns[i] = theta / pi;
+    }
+    const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(num_positions * p.half, 256), 1 << 20);
+    pkv::rope_table_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    PKV_CUDA(cudaGetLastError());
+    return PKV_OK;
+}
+
+int pkv_rope_and_cache(void* query_out, const void* query, const void* key, const void* value, int64_t query_stride,
+                       int64_t key_stride, int64_t value_stride, const void* q_norm_weight, const void* k_norm_weight,
+                       float eps, const float* cos_sin, int64_t max_position, int rotary_dim, int interleaved,
+                       const int64_t* positions, void* key_cache, void* value_cache, const int64_t* slot_mapping,
+                       int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                       int64_t num_blocks, int dtype, pkv_stream_t stream) {
+    return rope_impl<pkv::kPoolSame>(query_out, query, key, value, query_stride, key_stride, value_stride,
+                                     q_norm_weight, k_norm_weight, eps, cos_sin, max_position, rotary_dim, interleaved,
+                                     positions, key_cache, value_cache, slot_mapping, num_tokens, num_q_heads,
+                                     num_kv_heads, head_dim, block_size, num_blocks, dtype, 1.f, 1.f, stream);
+}
+
+int pkv_rope_and_cache_fp8(void* query_out, const void* query, const void* key, const void* value,
+                           int64_t query_stride, int64_t key_stride, int64_t value_stride, const void* q_norm_weight,
+                           const void* k_norm_weight, float eps, const float* cos_sin, int64_t max_position,
+                           int rotary_dim, int interleaved, const int64_t* positions, void* key_cache,
+                           void* value_cache, const int64_t* slot_mapping, int64_t num_tokens, int num_q_heads,
+                           int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, int dtype,
+                           float k_scale, float v_scale, pkv_stream_t stream) {
+    return rope_impl<pkv::kPoolE4M3>(query_out, query, key, value, query_stride, key_stride, value_stride,
+                                     q_norm_weight, k_norm_weight, eps, cos_sin, max_position, rotary_dim, interleaved,
+                                     positions, key_cache, value_cache, slot_mapping, num_tokens, num_q_heads,
+                                     num_kv_heads, head_dim, block_size, num_blocks, dtype, k_scale, v_scale, stream);
+}
+
+int pkv_rope_and_cache_int8(void* query_out, const void* query, const void* key, const void* value,
+                            int64_t query_stride, int64_t key_stride, int64_t value_stride, const void* q_norm_weight,
+                            const void* k_norm_weight, float eps, const float* cos_sin, int64_t max_position,
+                            int rotary_dim, int interleaved, const int64_t* positions, void* key_cache,
+                            void* value_cache, const int64_t* slot_mapping, int64_t num_tokens, int num_q_heads,
+                            int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, int dtype,
+                            pkv_stream_t stream) {
+    return rope_impl<pkv::kPoolInt8>(query_out, query, key, value, query_stride, key_stride, value_stride,
+                                     q_norm_weight, k_norm_weight, eps, cos_sin, max_position, rotary_dim, interleaved,
+                                     positions, key_cache, value_cache, slot_mapping, num_tokens, num_q_heads,
+                                     num_kv_heads, head_dim, block_size, num_blocks, dtype, 1.f, 1.f, stream);
+}
+
+int64_t pkv_int8_block_bytes(int block_size, int num_kv_heads, int head_dim) {
+    if (block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0) return PKV_EINVAL;
+    return (int64_t)block_size * num_kv_heads * ((int64_t)head_dim + 4);
+}
+
+int pkv_reshape_and_cache_int8(const void* key, const void* value, void* key_cache, void* value_cache,
+                               const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads, int head_dim,
+                               int block_size, int64_t num_blocks, int src_dtype, pkv_stream_t stream) {
+    int rc = rows_int8_check(key, value, key_cache, value_cache, slot_mapping, num_tokens, num_kv_heads, head_dim,
+                             block_size, num_blocks, src_dtype);
+    if (rc || num_tokens == 0) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t num_slots = num_blocks * block_size;
+    rc = check_slots(slot_mapping, num_tokens, num_slots, s);
+    if (rc) return rc;
+    auto launch = src_dtype == PKV_F32   ? launch_append_int8<float>
+                  : src_dtype == PKV_F16 ? launch_append_int8<__half>
+                                         : launch_append_int8<__nv_bfloat16>;
+    return launch(key, value, key_cache, value_cache, slot_mapping, num_tokens, num_kv_heads, head_dim, block_size,
+                  num_slots, s);
+}
+
+int pkv_read_cache_int8(void* key_out, void* value_out, const void* key_cache, const void* value_cache,
+                        const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads, int head_dim,
+                        int block_size, int64_t num_blocks, int dst_dtype, pkv_stream_t stream) {
+    int rc = rows_int8_check(key_out, value_out, key_cache, value_cache, slot_mapping, num_tokens, num_kv_heads,
+                             head_dim, block_size, num_blocks, dst_dtype);
+    if (rc || num_tokens == 0) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t num_slots = num_blocks * block_size;
+    rc = check_slots(slot_mapping, num_tokens, num_slots, s);
+    if (rc) return rc;
+    auto launch = dst_dtype == PKV_F32   ? launch_read_int8<float>
+                  : dst_dtype == PKV_F16 ? launch_read_int8<__half>
+                                         : launch_read_int8<__nv_bfloat16>;
+    return launch(key_out, value_out, key_cache, value_cache, slot_mapping, num_tokens, num_kv_heads, head_dim,
+                  block_size, num_slots, s);
+}
+
+}  // extern "C"

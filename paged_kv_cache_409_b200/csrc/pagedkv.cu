@@ -18,6 +18,7 @@
 #include "pagedkv.h"
 #include "ptx.cuh"
 #include "index_kernels.cuh"
+#include "row_kernels.cuh"
 #include "decode.cuh"
 #include "decode_mma.cuh"
 #include "decode_fp8.cuh"
@@ -1421,3 +1422,5 @@ extern "C" int pkv_paged_attention_decode_static_scratch(
                                       num_blocks, max_context_len, partition_size, dtype, scratch,
                                       need > 0 ? (size_t)PKV_STATIC_DECODE_SCRATCH_BYTES : 0, stream);
 }
+
+#include "api_rows.cuh"

@@ -1,0 +1,147 @@
+"""The row calls without a GPU: arguments in their places, refusals before any launch, a scale of frequencies."""
+import ctypes
+
+import pytest
+import torch
+
+import paged_kv_cache_409_b200 as pkv
+from paged_kv_cache_409_b200 import _binding
+from test_binding_marshalling import f32, mock  # noqa: F401
+
+EINVAL, EUNSUPPORTED = -1, -2
+
+
+def test_rope_arguments(mock):  # noqa: F811
+    T, Hq, Hkv, D, B, NB, R = 5, 8, 2, 64, 16, 7, 32
+    qkv = torch.zeros(T, (Hq + 2 * Hkv) * D, dtype=torch.bfloat16)
+    q, k, v = (qkv[:, : Hq * D].view(T, Hq, D), qkv[:, Hq * D: (Hq + Hkv) * D].view(T, Hkv, D),
+               qkv[:, (Hq + Hkv) * D:].view(T, Hkv, D))
+    out = torch.zeros(T, Hq, D, dtype=torch.bfloat16)
+    table, pos, slots = torch.zeros(99, R), torch.zeros(T, dtype=torch.int64), torch.zeros(T, dtype=torch.int64)
+    w = torch.zeros(D, dtype=torch.bfloat16)
+    kc, vc = torch.zeros(NB, B, Hkv, D, dtype=torch.bfloat16), torch.zeros(NB, B, Hkv, D, dtype=torch.bfloat16)
+    pkv.rope_and_cache(out, q, k, v, table, pos, kc, vc, slots, interleaved=True, q_norm_weight=w, eps=0.25, stream=3)
+    name, a = mock.last()
+    want = {"query_out": out.data_ptr(), "query": q.data_ptr(), "key": k.data_ptr(), "value": v.data_ptr(),
+            "query_stride": 768, "key_stride": 768, "value_stride": 768, "q_norm_weight": w.data_ptr(),
+            "k_norm_weight": 0, "eps": 0.25, "cos_sin": table.data_ptr(), "max_position": 99, "rotary_dim": R,
+            "interleaved": 1, "positions": pos.data_ptr(), "key_cache": kc.data_ptr(), "value_cache": vc.data_ptr(),
+            "slot_mapping": slots.data_ptr(), "num_tokens": T, "num_q_heads": Hq, "num_kv_heads": Hkv, "head_dim": D,
+            "block_size": B, "num_blocks": NB, "dtype": 2, "stream": 3}
+    assert name == "pkv_rope_and_cache" and a == want
+    p8 = [torch.zeros(NB, B, Hkv, D, dtype=torch.uint8) for _ in range(2)]
+    pkv.rope_and_cache_fp8(out, q, k, v, None, None, *p8, slots, 0.1, 0.2, k_norm_weight=w, stream=3)
+    name, a = mock.last()
+    assert name == "pkv_rope_and_cache_fp8"
+    assert a == {**want, "q_norm_weight": 0, "k_norm_weight": w.data_ptr(), "eps": f32(1e-6), "cos_sin": 0,
+                 "max_position": 0, "rotary_dim": 0, "interleaved": 0, "positions": 0, "key_cache": p8[0].data_ptr(),
+                 "value_cache": p8[1].data_ptr(), "k_scale": f32(0.1), "v_scale": f32(0.2)}
+    pi = [torch.zeros(NB, B, Hkv, D + 4, dtype=torch.uint8) for _ in range(2)]
+    pkv.rope_and_cache_int8(out[:1], q[:1], k[:1], v[:1], table, pos[:1], *pi, slots[:1], stream=3)
+    name, a = mock.last()
+    assert name == "pkv_rope_and_cache_int8"
+    assert (a["query_stride"], a["key_stride"], a["num_tokens"], a["head_dim"], a["num_blocks"]) == (512, 128, 1, D, NB)
+    pkv.reshape_and_cache_int8(k.contiguous(), v.contiguous(), *pi, slots, stream=3)
+    name, a = mock.last()
+    assert name == "pkv_reshape_and_cache_int8"
+    assert (a["key_cache"], a["value_cache"], a["num_tokens"], a["num_kv_heads"], a["head_dim"], a["block_size"],
+            a["num_blocks"], a["src_dtype"]) == (pi[0].data_ptr(), pi[1].data_ptr(), T, Hkv, D, B, NB, 2)
+    ko, vo = torch.zeros(T, Hkv, D), torch.zeros(T, Hkv, D)
+    pkv.read_cache_int8(ko, vo, *pi, slots, stream=3)
+    name, a = mock.last()
+    assert name == "pkv_read_cache_int8" and a["dst_dtype"] == 0 and a["key_out"] == ko.data_ptr()
+    pkv.rope_table(table, first_position=12, stream=3)
+    name, a = mock.last()
+    assert name == "pkv_rope_table" and (a["cos_sin"], a["first_position"], a["num_positions"]) == (table.data_ptr(), 12, 99)
+    assert pkv.int8_block_bytes(16, 2, 64) == 0  # the stand-in's answer
+    assert mock.last() == ("pkv_int8_block_bytes", {"block_size": 16, "num_kv_heads": 2, "head_dim": 64})
+
+
+def test_binding_refuses_what_does_not_fit_together(mock):  # noqa: F811
+    T, Hq, Hkv, D = 3, 4, 2, 64
+    q, k = torch.zeros(T, Hq, D), torch.zeros(T, Hkv, D)
+    pool, table = torch.zeros(4, 8, Hkv, D), torch.zeros(9, 32)
+    i = torch.zeros(T, dtype=torch.int64)
+
+    def call(**kw):
+        a = dict(query_out=q, query=q, key=k, value=k, cos_sin=table, positions=i, key_cache=pool, value_cache=pool,
+                 slot_mapping=i)
+        a.update(kw)
+        pkv.rope_and_cache(**a)
+
+    call()
+    for bad in (dict(key=k[:2]), dict(value=torch.zeros(T, Hkv, 32)), dict(query_out=q.half()), dict(key=k.half()),
+                dict(cos_sin=table.double()), dict(positions=i.int()), dict(positions=None), dict(slot_mapping=i[:2]),
+                dict(q_norm_weight=torch.zeros(32)), dict(k_norm_weight=torch.zeros(D).half()),
+                dict(key_cache=pool.half()), dict(value_cache=pool[:2]), dict(key=torch.zeros(T, D, Hkv).transpose(1, 2))):
+        with pytest.raises(ValueError):
+            call(**bad)
+    u8 = torch.zeros(4, 8, Hkv, D + 4, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        pkv.reshape_and_cache_int8(k, k, u8, u8[:2], i)
+    with pytest.raises(ValueError):
+        pkv.reshape_and_cache_int8(k, k, u8.int(), u8, i)
+    with pytest.raises(ValueError):
+        pkv.reshape_and_cache_int8(k, k[:2], u8, u8, i)
+    with pytest.raises(ValueError):
+        pkv.read_cache_int8(k, k.half(), u8, u8, i)
+    with pytest.raises(ValueError):
+        pkv.rope_table(table, scaling="other")
+    with pytest.raises(ValueError):
+        pkv.rope_table(table.double())
+
+
+def test_host_refusals():
+    """Statuses of the C calls for arguments they refuse; every pointer is made up and never read."""
+    from paged_kv_cache_409_b200 import build
+    build.build()
+    lib = pkv.load_library()
+    P = 1 << 20
+
+    def rope(fn, *tail, **kw):
+        a = dict(query_out=P, query=2 * P, key=3 * P, value=4 * P, qs=512, ks=128, vs=128, qw=0, kw=0, eps=1e-6, cos=5 * P,
+                 maxp=100, R=64, il=0, pos=6 * P, kc=7 * P, vc=8 * P, slots=9 * P, T=0, Hq=8, Hkv=2, D=64, B=16, NB=4, dt=1)
+        a.update(kw)
+        return fn(*a.values(), *tail, None)
+
+    same, fp8, i8 = lib.pkv_rope_and_cache, lib.pkv_rope_and_cache_fp8, lib.pkv_rope_and_cache_int8
+    assert rope(same) == 0 and rope(i8) == 0 and rope(fp8, 1.0, 1.0) == 0  # no token: nothing to do
+    for kw in (dict(dt=3), dict(dt=9), dict(D=60, R=0), dict(D=264), dict(R=20)):
+        assert rope(same, **kw) == EUNSUPPORTED, kw
+    for kw in (dict(T=-1), dict(Hq=0), dict(Hkv=0), dict(B=0), dict(NB=0), dict(R=72), dict(R=-8), dict(maxp=-1),
+               dict(eps=-1.0), dict(eps=float("nan"))):
+        assert rope(same, **kw) == EINVAL, kw
+    for kw in (dict(query=0), dict(query_out=0), dict(key=0), dict(value=0), dict(kc=0), dict(vc=0), dict(slots=0),
+               dict(cos=0), dict(pos=0), dict(qs=504), dict(ks=120), dict(vs=0), dict(qs=516), dict(key=3 * P + 8),
+               dict(kc=7 * P + 4), dict(qw=P + 2), dict(pos=6 * P + 4), dict(query_out=2 * P, qs=1024)):
+        assert rope(same, **{**dict(T=3), **kw}) == EINVAL, kw
+    assert rope(fp8, 0.0, 1.0) == EINVAL and rope(fp8, 1.0, float("nan")) == EINVAL
+    assert rope(fp8, 1.0, 1.0, D=72, R=0) == EUNSUPPORTED
+    assert rope(i8, D=72, R=0) == EUNSUPPORTED and rope(i8, B=1, Hkv=2) == EUNSUPPORTED
+
+    for fn in (lib.pkv_reshape_and_cache_int8, lib.pkv_read_cache_int8):
+        assert fn(P, P, P, P, P, 0, 2, 64, 16, 4, 1, None) == 0
+        assert fn(P, P, P, P, P, 3, 2, 64, 16, 4, 3, None) == EUNSUPPORTED
+        assert fn(P, P, P, P, P, 3, 2, 72, 16, 4, 1, None) == EUNSUPPORTED
+        assert fn(P, P, P, P, P, 3, 2, 272, 16, 4, 1, None) == EUNSUPPORTED
+        assert fn(P, P, P, P, P, 3, 1, 64, 2, 4, 1, None) == EUNSUPPORTED
+        assert fn(P, P, P, P, P, -3, 2, 64, 16, 4, 1, None) == EINVAL
+        assert fn(P, 0, P, P, P, 3, 2, 64, 16, 4, 1, None) == EINVAL
+        assert fn(P, P, P + 8, P, P, 3, 2, 64, 16, 4, 1, None) == EINVAL
+        assert fn(P, P, P, P, P + 4, 3, 2, 64, 16, 4, 1, None) == EINVAL
+    assert lib.pkv_int8_block_bytes(16, 8, 128) == 16 * 8 * 132 and lib.pkv_int8_block_bytes(0, 8, 128) == EINVAL
+
+    def table(first=0, n=0, ptr=P, **kw):
+        a = dict(base=1e4, factor=2.0, alpha=1.0, beta=4.0, attention_factor=1.0, original_max_position=100,
+                 rotary_dim=64, scaling=0)
+        a.update(kw)
+        return lib.pkv_rope_table(ptr, first, n, ctypes.byref(_binding.RopeSpec(*a.values())), None)
+
+    assert table() == 0
+    for kw in (dict(scaling=4), dict(scaling=-1), dict(rotary_dim=60), dict(rotary_dim=264), dict(rotary_dim=8, scaling=2)):
+        assert table(**kw) == EUNSUPPORTED, kw
+    for kw in (dict(first=-1), dict(n=-1), dict(first=1 << 40, n=1), dict(base=0.0), dict(rotary_dim=0),
+               dict(attention_factor=float("inf")), dict(scaling=1, factor=0.0), dict(scaling=3, alpha=4.0),
+               dict(scaling=3, original_max_position=0), dict(n=3, ptr=0), dict(n=3, ptr=P + 4)):
+        assert table(**kw) == EINVAL, kw
+    assert lib.pkv_rope_table(P, 0, 0, None, None) == EINVAL
