@@ -356,6 +356,30 @@ int pkv_paged_attention_decode_fp8(void* out, const void* query, const void* key
                                    size_t workspace_bytes, pkv_stream_t stream);
 
 /*
+ * Decode attention over int8 pools: the same result as
+ * pkv_paged_attention_decode with every pool row read as its scale times
+ * (code - 128).  The query is used as a 16-bit integer row (half a step is
+ * 2^-16 of its largest element); products with the codes are exact, weights
+ * are f16 relative to the largest weight times V scale, sums are fp32.
+ *
+ *   query, out      device [num_seqs, num_q_heads, head_dim], dtype F16 or BF16
+ *   key_cache,
+ *   value_cache     device, num_blocks blocks of pkv_int8_block_bytes
+ * Every other argument, the workspace (pkv_decode_workspace_size; partition
+ * sizes from pkv_decode_partition_size with dtype PKV_INT8) and the error
+ * behaviour are those of pkv_paged_attention_decode.  A NaN or infinity in a
+ * query row, or a row of scale NaN inside the context, gives NaN.
+ * Supported: head_dim in {64, 128}; block_size in {8, 16, 32}; num_q_heads /
+ * num_kv_heads in {1, 2, 4, 8}.
+ */
+int pkv_paged_attention_decode_int8(void* out, const void* query, const void* key_cache, const void* value_cache,
+                                    const int32_t* block_tables, const int32_t* context_lens, float scale,
+                                    int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                    int max_blocks_per_seq, int64_t num_blocks, int max_context_len,
+                                    int partition_size, int dtype, void* workspace, size_t workspace_bytes,
+                                    pkv_stream_t stream);
+
+/*
  * One decode step in one call: pkv_reshape_and_cache of the step's new tokens
  * (new_keys / new_values [num_new_tokens, num_kv_heads, head_dim] in dtype, at
  * slot_mapping), then pkv_paged_attention_decode over the same pools.  Source:
@@ -392,6 +416,16 @@ int pkv_paged_attention_decode_step_fp8(const void* new_keys, const void* new_va
                                         int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
                                         int64_t num_blocks, int max_context_len, int partition_size, int dtype,
                                         void* workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/* The same step over int8 pools: pkv_reshape_and_cache_int8 (new tokens in
+ * dtype), then pkv_paged_attention_decode_int8, launched as above. */
+int pkv_paged_attention_decode_step_int8(const void* new_keys, const void* new_values, const int64_t* slot_mapping,
+                                         int64_t num_new_tokens, void* out, const void* query, void* key_cache,
+                                         void* value_cache, const int32_t* block_tables, const int32_t* context_lens,
+                                         float scale, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                         int block_size, int max_blocks_per_seq, int64_t num_blocks,
+                                         int max_context_len, int partition_size, int dtype, void* workspace,
+                                         size_t workspace_bytes, pkv_stream_t stream);
 
 /* Workspace bytes pkv_paged_attention_decode needs for these sizes (0 when
  * partition_size == 0 or max_context_len <= partition_size). */

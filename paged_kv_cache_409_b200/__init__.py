@@ -22,8 +22,10 @@ from ._binding import (  # noqa: F401
     load_library,
     paged_attention_decode,
     paged_attention_decode_fp8,
+    paged_attention_decode_int8,
     paged_attention_decode_step,
     paged_attention_decode_step_fp8,
+    paged_attention_decode_step_int8,
     paged_attention_decode_multi,
     paged_attention_decode_multi_step,
     paged_attention_prefill_chunk,

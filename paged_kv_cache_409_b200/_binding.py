@@ -60,6 +60,8 @@ EXPORTED = (
     "pkv_int8_block_bytes",
     "pkv_reshape_and_cache_int8",
     "pkv_read_cache_int8",
+    "pkv_paged_attention_decode_int8",
+    "pkv_paged_attention_decode_step_int8",
 )
 
 
@@ -130,6 +132,8 @@ def load_library():
     lib.pkv_int8_block_bytes.argtypes = [I, I, I]
     lib.pkv_int8_block_bytes.restype = I64
     lib.pkv_reshape_and_cache_int8.argtypes = [P, P, P, P, P, I64, I, I, I, I64, I, P]
+    lib.pkv_paged_attention_decode_int8.argtypes = lib.pkv_paged_attention_decode.argtypes
+    lib.pkv_paged_attention_decode_step_int8.argtypes = lib.pkv_paged_attention_decode_step.argtypes
     lib.pkv_read_cache_int8.argtypes = [P, P, P, P, P, I64, I, I, I, I64, I, P]
     for name in ("pkv_reshape_and_cache", "pkv_reshape_and_cache_fp8", "pkv_paged_attention_decode_fp8",
                  "pkv_copy_blocks", "pkv_swap_blocks", "pkv_paged_attention_decode",
@@ -139,7 +143,8 @@ def load_library():
                  "pkv_decode_multi_partition_size", "pkv_paged_attention_decode_step",
                  "pkv_paged_attention_decode_step_fp8", "pkv_set_wait_limit_ns", "pkv_rope_table",
                  "pkv_rope_and_cache", "pkv_rope_and_cache_fp8", "pkv_rope_and_cache_int8",
-                 "pkv_reshape_and_cache_int8", "pkv_read_cache_int8"):
+                 "pkv_reshape_and_cache_int8", "pkv_read_cache_int8", "pkv_paged_attention_decode_int8",
+                 "pkv_paged_attention_decode_step_int8"):
         getattr(lib, name).restype = I
     _lib = lib
     return lib
@@ -675,6 +680,57 @@ def read_cache_int8(key_out, value_out, key_cache, value_cache, slot_mapping, st
                                  _here(slot_mapping, "slot_mapping"), T, H, D, B, NB, _code(key_out), _stream(stream))
     _ok(rc, "read_cache_int8")
     return key_out, value_out
+
+
+def _int8_decode_args(out, query, key_cache, value_cache, block_tables, context_lens, max_context_len, partition_size,
+                      workspace, total_context_tokens):
+    """The arguments shared by the int8 decode and its step: (out, query, pools, tables) pointers, the sizes, the
+    partition and the workspace."""
+    (NB, B, Hkv, D), k, v = _int8_pools(key_cache, value_cache)
+    S, Hq, Dq = query.shape
+    if Dq != D or out.shape != query.shape or out.dtype != query.dtype:
+        raise ValueError("out and query must be [num_seqs, num_q_heads, head_dim] of the pools, in one dtype")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise ValueError("block_tables and context_lens must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq] and context_lens [num_seqs]")
+    part, ws_ptr, ws_bytes = _decode_workspace(S, Hq, Hkv, D, B, max_context_len, INT8, partition_size, workspace,
+                                               query.device, total_context_tokens)
+    return ((_here(out, "out"), _here(query, "query"), k, v, _here(block_tables, "block_tables"),
+             _here(context_lens, "context_lens")),
+            (S, Hq, Hkv, D, B, block_tables.shape[1], NB, int(max_context_len), part, _code(query), ws_ptr, ws_bytes))
+
+
+def paged_attention_decode_int8(out, query, key_cache, value_cache, block_tables, context_lens, scale,
+                                max_context_len, partition_size=None, workspace=None, stream=None,
+                                total_context_tokens=0):
+    """Decode attention over int8 pools (uint8 ``[NB, B, Hkv, D + 4]``); ``out``/``query`` ``[S, Hq, D]`` in fp16 or
+    bf16, the other arguments as for :func:`paged_attention_decode`."""
+    lib = load_library()
+    ptrs, sizes = _int8_decode_args(out, query, key_cache, value_cache, block_tables, context_lens, max_context_len,
+                                    partition_size, workspace, total_context_tokens)
+    _ok(lib.pkv_paged_attention_decode_int8(*ptrs, float(scale), *sizes, _stream(stream)),
+        "paged_attention_decode_int8")
+    return out
+
+
+def paged_attention_decode_step_int8(new_keys, new_values, slot_mapping, out, query, key_cache, value_cache,
+                                     block_tables, context_lens, scale, max_context_len, partition_size=None,
+                                     workspace=None, stream=None, total_context_tokens=0):
+    """The decode step over int8 pools: ``reshape_and_cache_int8`` then ``paged_attention_decode_int8``."""
+    lib = load_library()
+    ptrs, sizes = _int8_decode_args(out, query, key_cache, value_cache, block_tables, context_lens, max_context_len,
+                                    partition_size, workspace, total_context_tokens)
+    T, rows = slot_mapping.numel(), (slot_mapping.numel(), *sizes[2:4])
+    if slot_mapping.dtype != torch.int64:
+        raise ValueError("slot_mapping must be int64")
+    if new_keys.shape != rows or new_values.shape != rows or not new_keys.dtype == new_values.dtype == query.dtype:
+        raise ValueError("new_keys and new_values must be [tokens, num_kv_heads, head_dim] in the query's dtype")
+    rc = lib.pkv_paged_attention_decode_step_int8(_here(new_keys, "new_keys"), _here(new_values, "new_values"),
+                                                  _here(slot_mapping, "slot_mapping"), T, *ptrs, float(scale), *sizes,
+                                                  _stream(stream))
+    _ok(rc, "paged_attention_decode_step_int8")
+    return out
 
 
 def get_device_error(stream=None) -> int:

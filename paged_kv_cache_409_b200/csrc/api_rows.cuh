@@ -270,4 +270,43 @@ int pkv_read_cache_int8(void* key_out, void* value_out, const void* key_cache, c
                   block_size, num_slots, s);
 }
 
+int pkv_paged_attention_decode_int8(void* out, const void* query, const void* key_cache, const void* value_cache,
+                                    const int32_t* block_tables, const int32_t* context_lens, float scale,
+                                    int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                    int max_blocks_per_seq, int64_t num_blocks, int max_context_len,
+                                    int partition_size, int dtype, void* workspace, size_t workspace_bytes,
+                                    pkv_stream_t stream) {
+    return decode_impl(out, query, key_cache, value_cache, block_tables, context_lens, scale, num_seqs, num_q_heads,
+                       num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, max_context_len,
+                       partition_size, dtype, PKV_INT8, 1.f, 1.f, workspace, workspace_bytes, stream);
+}
+
+int pkv_paged_attention_decode_step_int8(const void* new_keys, const void* new_values, const int64_t* slot_mapping,
+                                         int64_t num_new_tokens, void* out, const void* query, void* key_cache,
+                                         void* value_cache, const int32_t* block_tables, const int32_t* context_lens,
+                                         float scale, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                         int block_size, int max_blocks_per_seq, int64_t num_blocks,
+                                         int max_context_len, int partition_size, int dtype, void* workspace,
+                                         size_t workspace_bytes, pkv_stream_t stream) {
+    // Every check of both calls before the first launch, so that a refused
+    // step has changed nothing.
+    int rc = decode_check(out, query, key_cache, value_cache, block_tables, context_lens, scale, num_seqs,
+                          num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks,
+                          max_context_len, partition_size, dtype, PKV_INT8);
+    if (rc) return rc;
+    rc = decode_workspace_check(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                                partition_size, workspace, workspace_bytes);
+    if (rc) return rc;
+    rc = rows_int8_check(new_keys, new_values, key_cache, value_cache, slot_mapping, num_new_tokens, num_kv_heads,
+                         head_dim, block_size, num_blocks, dtype);
+    if (rc) return rc;
+    rc = pkv_reshape_and_cache_int8(new_keys, new_values, key_cache, value_cache, slot_mapping, num_new_tokens,
+                                    num_kv_heads, head_dim, block_size, num_blocks, dtype, stream);
+    if (rc) return rc;
+    return decode_impl(out, query, key_cache, value_cache, block_tables, context_lens, scale, num_seqs, num_q_heads,
+                       num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, max_context_len,
+                       partition_size, dtype, PKV_INT8, 1.f, 1.f, workspace, workspace_bytes, stream,
+                       /*pdl=*/num_new_tokens > 0);
+}
+
 }  // extern "C"

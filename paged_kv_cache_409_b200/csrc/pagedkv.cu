@@ -22,6 +22,7 @@
 #include "decode.cuh"
 #include "decode_mma.cuh"
 #include "decode_fp8.cuh"
+#include "decode_int8.cuh"
 #include "decode_multi.cuh"
 #include "prefill.cuh"
 
@@ -109,6 +110,33 @@ int make_pool_map(CUtensorMap* map, const void* pool, int dtype, int64_t num_blo
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         snprintf(g_last_cuda_error, sizeof g_last_cuda_error, "cuTensorMapEncodeTiled(pool) failed: %d", (int)r);
+        return PKV_ECUDA;
+    }
+    return PKV_OK;
+}
+
+// The codes of an int8 pool, [num_blocks][block_size, num_kv_heads, head_dim]
+// with the scales between blocks: one box = one block x one KV head, swizzled
+// over the row's 64 or 128 bytes.
+int make_int8_map(CUtensorMap* map, const void* pool, int64_t num_blocks, int block_size, int num_kv_heads,
+                  int head_dim) {
+    auto fn = encode_fn();
+    if (!fn) {
+        snprintf(g_last_cuda_error, sizeof g_last_cuda_error, "cuTensorMapEncodeTiled unavailable");
+        return PKV_ECUDA;
+    }
+    cuuint64_t dims[4] = {(cuuint64_t)head_dim, (cuuint64_t)num_kv_heads, (cuuint64_t)block_size,
+                          (cuuint64_t)num_blocks};
+    cuuint64_t strides[3] = {(cuuint64_t)head_dim, (cuuint64_t)num_kv_heads * head_dim,
+                             (cuuint64_t)pkv::int8_block_bytes(block_size, num_kv_heads, head_dim)};
+    cuuint32_t box[4] = {(cuuint32_t)head_dim, 1, (cuuint32_t)block_size, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pool), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        snprintf(g_last_cuda_error, sizeof g_last_cuda_error, "cuTensorMapEncodeTiled(int8 pool) failed: %d", (int)r);
         return PKV_ECUDA;
     }
     return PKV_OK;
@@ -342,6 +370,41 @@ int decode_fp8_by_block(int block_size, int group, const pkv::DecodeParams& prm,
     }
 }
 
+// int8 pools: units of at least 16 tokens, two stages per warp.
+template <typename T, int D, int B, int G>
+int launch_decode_int8(const pkv::DecodeParams& prm, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                       const Launch& ln) {
+    constexpr int NW = 4, NST = 2;
+    constexpr int U = B < 16 ? 16 / B : 1;
+    using C = pkv::DecodeInt8Cfg<D, B, G, NST, NW, U>;
+    static size_t configured[64] = {};
+    return launch_decode_kernel(pkv::paged_decode_int8_kernel<T, D, B, G, NST, NW, U>,
+                                C::smem_bytes(prm.partition_blocks), NW * 32, prm, tk, tv, grid, ln, configured);
+}
+
+template <typename T, int D, int B>
+int decode_int8_by_group(int group, const pkv::DecodeParams& prm, const CUtensorMap& tk, const CUtensorMap& tv,
+                         int grid, const Launch& ln) {
+    switch (group) {
+        case 1: return launch_decode_int8<T, D, B, 1>(prm, tk, tv, grid, ln);
+        case 2: return launch_decode_int8<T, D, B, 2>(prm, tk, tv, grid, ln);
+        case 4: return launch_decode_int8<T, D, B, 4>(prm, tk, tv, grid, ln);
+        case 8: return launch_decode_int8<T, D, B, 8>(prm, tk, tv, grid, ln);
+        default: return PKV_EUNSUPPORTED;
+    }
+}
+
+template <typename T, int D>
+int decode_int8_by_block(int block_size, int group, const pkv::DecodeParams& prm, const CUtensorMap& tk,
+                         const CUtensorMap& tv, int grid, const Launch& ln) {
+    switch (block_size) {
+        case 8: return decode_int8_by_group<T, D, 8>(group, prm, tk, tv, grid, ln);
+        case 16: return decode_int8_by_group<T, D, 16>(group, prm, tk, tv, grid, ln);
+        case 32: return decode_int8_by_group<T, D, 32>(group, prm, tk, tv, grid, ln);
+        default: return PKV_EUNSUPPORTED;
+    }
+}
+
 // ------------------------------------------------------------ multi-token decode dispatch
 // Persistent: as many CTAs as fit on the device at once (one per SM at
 // head_dim 128), at most one per item.
@@ -422,9 +485,10 @@ int decode_check(const void* out, const void* query, const void* key_cache, cons
                  const int32_t* block_tables, const int32_t* context_lens, float scale, int num_seqs,
                  int num_q_heads, int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
                  int64_t num_blocks, int max_context_len, int partition_size, int dtype, int kv_dtype) {
-    const bool fp8 = kv_dtype == PKV_FP8_E4M3;
-    if (!query_type(dtype) || (kv_dtype != dtype && !fp8)) return PKV_EUNSUPPORTED;
+    const bool fp8 = kv_dtype == PKV_FP8_E4M3, int8 = kv_dtype == PKV_INT8;
+    if (!query_type(dtype) || (kv_dtype != dtype && !fp8 && !int8)) return PKV_EUNSUPPORTED;
     if (fp8 && (dtype == PKV_F32 || head_dim != 128)) return PKV_EUNSUPPORTED;
+    if (int8 && dtype == PKV_F32) return PKV_EUNSUPPORTED;
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 ||
         max_context_len < 0 || partition_size < 0 || !std::isfinite(scale))
         return PKV_EINVAL;
@@ -496,7 +560,7 @@ int reshape_fp8_check(const void* key, const void* value, const void* key_cache,
 }
 
 // Decode with the query / output in `dtype` and the pools in `kv_dtype`
-// (the same 16/32-bit type, or FP8 E4M3 with its two scales).
+// (the same 16/32-bit type, FP8 E4M3 with its two scales, or 8-bit rows).
 int decode_impl(void* out, const void* query, const void* key_cache, const void* value_cache,
                 const int32_t* block_tables, const int32_t* context_lens, float scale, int num_seqs, int num_q_heads,
                 int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks,
@@ -506,7 +570,7 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
                                    num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks,
                                    max_context_len, partition_size, dtype, kv_dtype);
     if (check || num_seqs == 0) return check;
-    const bool fp8 = kv_dtype == PKV_FP8_E4M3;
+    const bool fp8 = kv_dtype == PKV_FP8_E4M3, int8 = kv_dtype == PKV_INT8;
     const int group = num_q_heads / num_kv_heads;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
 
@@ -528,10 +592,14 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
         if (rc) return rc;
     }
 
+    auto make_map = [&](CUtensorMap* map, const void* pool) {
+        return int8 ? make_int8_map(map, pool, num_blocks, block_size, num_kv_heads, head_dim)
+                    : make_pool_map(map, pool, kv_dtype, num_blocks, block_size, num_kv_heads, head_dim);
+    };
     CUtensorMap tk, tv;
-    int rc = make_pool_map(&tk, key_cache, kv_dtype, num_blocks, block_size, num_kv_heads, head_dim);
+    int rc = make_map(&tk, key_cache);
     if (rc) return rc;
-    rc = make_pool_map(&tv, value_cache, kv_dtype, num_blocks, block_size, num_kv_heads, head_dim);
+    rc = make_map(&tv, value_cache);
     if (rc) return rc;
 
     pkv::DecodeParams prm;
@@ -553,9 +621,20 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
     prm.num_blocks = num_blocks;
     prm.partition_blocks = (int)pb;
     prm.num_partitions = (int)parts;
+    const int64_t codes = (int64_t)block_size * num_kv_heads * head_dim;
+    prm.k_scales = int8 ? static_cast<const uint8_t*>(key_cache) + codes : nullptr;
+    prm.v_scales = int8 ? static_cast<const uint8_t*>(value_cache) + codes : nullptr;
+    prm.block_bytes = pkv::int8_block_bytes(block_size, num_kv_heads, head_dim);
 
     const Launch ln{s, pdl};
-    if (fp8) {
+    if (int8) {
+        auto by_dim = [&](auto q) {
+            using T = decltype(q);
+            return head_dim == 64 ? decode_int8_by_block<T, 64>(block_size, group, prm, tk, tv, (int)grid, ln)
+                                  : decode_int8_by_block<T, 128>(block_size, group, prm, tk, tv, (int)grid, ln);
+        };
+        rc = dtype == PKV_F16 ? by_dim(__half()) : by_dim(__nv_bfloat16());
+    } else if (fp8) {
         rc = dtype == PKV_F16 ? decode_fp8_by_block<__half>(block_size, group, prm, tk, tv, (int)grid, ln)
                               : decode_fp8_by_block<__nv_bfloat16>(block_size, group, prm, tk, tv, (int)grid, ln);
     } else {
@@ -768,7 +847,8 @@ size_t pkv_decode_workspace_size(int num_seqs, int num_q_heads, int head_dim, in
 int pkv_decode_partition_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                               int max_context_len, int64_t total_context_tokens, int dtype) {
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || head_dim <= 0 ||
-        block_size <= 0 || max_context_len < 0 || total_context_tokens < 0 || !elem_bytes(dtype))
+        block_size <= 0 || max_context_len < 0 || total_context_tokens < 0 ||
+        (!elem_bytes(dtype) && dtype != PKV_INT8))
         return PKV_EINVAL;
     (void)head_dim;
     const int64_t pairs = (int64_t)num_seqs * num_kv_heads;
@@ -809,7 +889,7 @@ int pkv_decode_partition_size(int num_seqs, int num_q_heads, int num_kv_heads, i
         // 8 KV heads with 8 query heads each (whose merge moves 8x the
         // partials), are fastest unsplit.
         const int64_t waves = 22 * (int64_t)sm_count();
-        if (dtype == PKV_FP8_E4M3 && num_q_heads == num_kv_heads && pairs < waves) {
+        if ((dtype == PKV_FP8_E4M3 || dtype == PKV_INT8) && num_q_heads == num_kv_heads && pairs < waves) {
             const double per_part = (double)num_kv_heads * total_context_tokens / (double)(waves - pairs / 2);
             return round_ps(std::max<int64_t>((int64_t)std::ceil(per_part), 512));
         }

@@ -145,3 +145,58 @@ def test_host_refusals():
                dict(scaling=3, original_max_position=0), dict(n=3, ptr=0), dict(n=3, ptr=P + 4)):
         assert table(**kw) == EINVAL, kw
     assert lib.pkv_rope_table(P, 0, 0, None, None) == EINVAL
+
+
+def test_decode_int8_arguments(mock):  # noqa: F811
+    S, Hq, Hkv, D, B, NB, MB = 4, 16, 4, 64, 32, 19, 3
+    q = torch.zeros(S, Hq, D, dtype=torch.bfloat16)
+    out = torch.zeros_like(q)
+    kc, vc = (torch.zeros(NB, B, Hkv, D + 4, dtype=torch.uint8) for _ in range(2))
+    bt, cl = torch.zeros(S, MB, dtype=torch.int32), torch.zeros(S, dtype=torch.int32)
+    pkv.paged_attention_decode_int8(out, q, kc, vc, bt, cl, 0.1, 90, partition_size=0, stream=2)
+    name, a = mock.last()
+    want = {"out": out.data_ptr(), "query": q.data_ptr(), "key_cache": kc.data_ptr(), "value_cache": vc.data_ptr(),
+            "block_tables": bt.data_ptr(), "context_lens": cl.data_ptr(), "scale": f32(0.1), "num_seqs": S,
+            "num_q_heads": Hq, "num_kv_heads": Hkv, "head_dim": D, "block_size": B, "max_blocks_per_seq": MB,
+            "num_blocks": NB, "max_context_len": 90, "partition_size": 0, "dtype": 2, "workspace": 0,
+            "workspace_bytes": 0, "stream": 2}
+    assert name == "pkv_paged_attention_decode_int8" and a == want
+    kn, vn, sm = torch.zeros(3, Hkv, D).bfloat16(), torch.zeros(3, Hkv, D).bfloat16(), torch.zeros(3, dtype=torch.int64)
+    pkv.paged_attention_decode_step_int8(kn, vn, sm, out, q, kc, vc, bt, cl, 0.1, 90, partition_size=0, stream=2)
+    name, a = mock.last()
+    assert name == "pkv_paged_attention_decode_step_int8"
+    assert a == {**want, "new_keys": kn.data_ptr(), "new_values": vn.data_ptr(), "slot_mapping": sm.data_ptr(),
+                 "num_new_tokens": 3}
+    for bad in (dict(query=q[:, :, :32]), dict(out=out.half()), dict(block_tables=bt.long()), dict(context_lens=cl[:2]),
+                dict(block_tables=bt[:2]), dict(key_cache=kc[:3]), dict(key_cache=kc.half())):
+        kw = dict(out=out, query=q, key_cache=kc, value_cache=vc, block_tables=bt, context_lens=cl)
+        with pytest.raises(ValueError):
+            pkv.paged_attention_decode_int8(**{**kw, **bad}, scale=0.1, max_context_len=90)
+
+
+def test_decode_int8_refusals():
+    from paged_kv_cache_409_b200 import build
+    build.build()
+    lib = pkv.load_library()
+    P = 1 << 20
+
+    def dec(fn=lib.pkv_paged_attention_decode_int8, head=(), **kw):
+        a = dict(out=P, q=P, kc=P, vc=P, bt=P, cl=P, scale=0.1, S=0, Hq=4, Hkv=2, D=64, B=16, MB=4, NB=8, mx=64, part=0,
+                 dt=1, ws=0, wb=0)
+        a.update(kw)
+        return fn(*head, *a.values(), None)
+
+    assert dec() == 0
+    for kw in (dict(dt=0), dict(dt=3), dict(dt=4), dict(D=96), dict(D=256), dict(B=64), dict(Hq=6), dict(Hq=32),
+               dict(S=1, MB=5000, mx=16 * 4097)):
+        assert dec(**kw) == EUNSUPPORTED, kw
+    for kw in (dict(S=-1), dict(Hq=5), dict(NB=0), dict(MB=0), dict(scale=float("nan")), dict(part=8), dict(mx=-1),
+               dict(S=1, q=0), dict(S=1, kc=P + 8), dict(S=1, cl=P + 2)):
+        assert dec(**kw) == EINVAL, kw
+    assert dec(S=1, part=16) == -5 and dec(S=1, part=16, ws=P, wb=100) == -5
+    step = lib.pkv_paged_attention_decode_step_int8
+    assert dec(step, (P, P, P, 0)) == 0
+    assert dec(step, (P, 0, P, 3)) == EINVAL and dec(step, (P, P, P, -1)) == EINVAL
+    assert dec(step, (P, P, P, 0), dt=0) == EUNSUPPORTED
+    assert pkv.decode_partition_size(64, 32, 32, 128, 16, 2048, pkv.INT8) == 0
+    assert lib.pkv_paged_attention_decode(P, P, P, P, P, P, 0.1, 1, 4, 2, 64, 16, 4, 8, 64, 0, 4, None, 0, None) == -2
