@@ -507,6 +507,24 @@ int pkv_paged_attention_prefill_chunk_fp8(void* out, const void* query, const vo
                                           int64_t num_blocks, int dtype, void* workspace, size_t workspace_bytes,
                                           pkv_stream_t stream);
 
+/*
+ * Chunked prefill over int8 pools: pkv_paged_attention_prefill_chunk with every
+ * pool row read as its scale times (code - 128).  The rows are widened inside
+ * the kernel, to f16 (half a step, 2^-11, of an element; 2^-25 below 2^-14):
+ * no workspace.  Both products run in f16 with fp32 accumulation, so |query|
+ * must stay below 65504; a row beyond that (scale above 511.75), like one of
+ * scale NaN, gives NaN to the query rows that see it, and to no others.
+ * Supported: dtype in {F16, BF16}, head_dim in {64, 128}, block_size in {8, 16,
+ * 32}, num_q_heads / num_kv_heads in {1, 2, 4, 8}.  Everything else is as
+ * there; the same call verifies a few draft tokens per sequence.
+ */
+int pkv_paged_attention_prefill_chunk_int8(void* out, const void* query, const void* key_cache,
+                                           const void* value_cache, const int32_t* block_tables,
+                                           const int32_t* seq_lens, const int32_t* query_start_loc, int num_chunks,
+                                           int64_t total_q_tokens, int max_q_len, float scale, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                                           int64_t num_blocks, int dtype, pkv_stream_t stream);
+
 /* Workspace bytes of pkv_paged_attention_prefill_chunk_fp8: two f16 scratch
  * pools of num_chunks * max_blocks_per_seq blocks, their table, and (bf16
  * queries) the f16 query. */

@@ -30,6 +30,7 @@ from ._binding import (  # noqa: F401
     paged_attention_decode_multi_step,
     paged_attention_prefill_chunk,
     paged_attention_prefill_chunk_fp8,
+    paged_attention_prefill_chunk_int8,
     read_cache_int8,
     reshape_and_cache,
     reshape_and_cache_fp8,

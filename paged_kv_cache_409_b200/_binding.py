@@ -62,6 +62,7 @@ EXPORTED = (
     "pkv_read_cache_int8",
     "pkv_paged_attention_decode_int8",
     "pkv_paged_attention_decode_step_int8",
+    "pkv_paged_attention_prefill_chunk_int8",
 )
 
 
@@ -134,6 +135,7 @@ def load_library():
     lib.pkv_reshape_and_cache_int8.argtypes = [P, P, P, P, P, I64, I, I, I, I64, I, P]
     lib.pkv_paged_attention_decode_int8.argtypes = lib.pkv_paged_attention_decode.argtypes
     lib.pkv_paged_attention_decode_step_int8.argtypes = lib.pkv_paged_attention_decode_step.argtypes
+    lib.pkv_paged_attention_prefill_chunk_int8.argtypes = lib.pkv_paged_attention_prefill_chunk.argtypes
     lib.pkv_read_cache_int8.argtypes = [P, P, P, P, P, I64, I, I, I, I64, I, P]
     for name in ("pkv_reshape_and_cache", "pkv_reshape_and_cache_fp8", "pkv_paged_attention_decode_fp8",
                  "pkv_copy_blocks", "pkv_swap_blocks", "pkv_paged_attention_decode",
@@ -144,7 +146,7 @@ def load_library():
                  "pkv_paged_attention_decode_step_fp8", "pkv_set_wait_limit_ns", "pkv_rope_table",
                  "pkv_rope_and_cache", "pkv_rope_and_cache_fp8", "pkv_rope_and_cache_int8",
                  "pkv_reshape_and_cache_int8", "pkv_read_cache_int8", "pkv_paged_attention_decode_int8",
-                 "pkv_paged_attention_decode_step_int8"):
+                 "pkv_paged_attention_decode_step_int8", "pkv_paged_attention_prefill_chunk_int8"):
         getattr(lib, name).restype = I
     _lib = lib
     return lib
@@ -730,6 +732,29 @@ def paged_attention_decode_step_int8(new_keys, new_values, slot_mapping, out, qu
                                                   _here(slot_mapping, "slot_mapping"), T, *ptrs, float(scale), *sizes,
                                                   _stream(stream))
     _ok(rc, "paged_attention_decode_step_int8")
+    return out
+
+
+def paged_attention_prefill_chunk_int8(out, query, key_cache, value_cache, block_tables, seq_lens, query_start_loc,
+                                       max_q_len, scale, stream=None):
+    """Causal chunked prefill over int8 pools (uint8 ``[NB, B, Hkv, D + 4]``); ``out``/``query`` packed
+    ``[sum n_r, Hq, D]`` in fp16 or bf16."""
+    lib = load_library()
+    (NB, B, Hkv, D), k, v = _int8_pools(key_cache, value_cache)
+    Tq, Hq, Dq = query.shape
+    R = seq_lens.numel()
+    if Dq != D or out.shape != query.shape or out.dtype != query.dtype:
+        raise ValueError("out and query must be [tokens, num_q_heads, head_dim] of the pools, in one dtype")
+    for t, name in ((block_tables, "block_tables"), (seq_lens, "seq_lens"), (query_start_loc, "query_start_loc")):
+        if t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != R or query_start_loc.numel() != R + 1:
+        raise ValueError("block_tables must be [chunks, max_blocks_per_seq] and query_start_loc [chunks + 1]")
+    rc = lib.pkv_paged_attention_prefill_chunk_int8(
+        _here(out, "out"), _here(query, "query"), k, v, _here(block_tables, "block_tables"),
+        _here(seq_lens, "seq_lens"), _here(query_start_loc, "query_start_loc"), R, Tq, int(max_q_len), float(scale),
+        Hq, Hkv, D, B, block_tables.shape[1], NB, _code(query), _stream(stream))
+    _ok(rc, "paged_attention_prefill_chunk_int8")
     return out
 
 

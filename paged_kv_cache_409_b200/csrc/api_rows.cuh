@@ -77,6 +77,40 @@ int launch_rope(const pkv::RopeRowsParams& p, cudaStream_t s) {
     return PKV_OK;
 }
 
+template <typename T, int D, int G>
+int launch_prefill_int8(const pkv::PrefillInt8Params& prm, const CUtensorMap& tq, const CUtensorMap& tk,
+                        const CUtensorMap& tv, int grid, cudaStream_t s) {
+    using C = pkv::PrefillInt8Cfg<D, G>;
+    auto kern = pkv::paged_prefill_int8_kernel<T, D, G>;
+    int dev = 0;
+    PKV_CUDA(cudaGetDevice(&dev));
+    static bool configured[64] = {};
+    if (!configured[dev & 63]) {
+        // the softmax threads' share (208) comes out of what the block is
+        // launched with: 512 threads x 128 registers, no fewer
+        cudaFuncAttributes a;
+        PKV_CUDA(cudaFuncGetAttributes(&a, kern));
+        if (a.numRegs < 128) return PKV_EUNSUPPORTED;
+        PKV_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+        configured[dev & 63] = true;
+    }
+    kern<<<grid, pkv::kPrefillInt8Threads, C::SMEM, s>>>(prm, tq, tk, tv);
+    PKV_CUDA(cudaGetLastError());
+    return PKV_OK;
+}
+
+template <typename T, int D>
+int prefill_int8_by_group(int group, const pkv::PrefillInt8Params& prm, const CUtensorMap& tq, const CUtensorMap& tk,
+                          const CUtensorMap& tv, int grid, cudaStream_t s) {
+    switch (group) {
+        case 1: return launch_prefill_int8<T, D, 1>(prm, tq, tk, tv, grid, s);
+        case 2: return launch_prefill_int8<T, D, 2>(prm, tq, tk, tv, grid, s);
+        case 4: return launch_prefill_int8<T, D, 4>(prm, tq, tk, tv, grid, s);
+        case 8: return launch_prefill_int8<T, D, 8>(prm, tq, tk, tv, grid, s);
+        default: return PKV_EUNSUPPORTED;
+    }
+}
+
 template <int kPool>
 int rope_impl(void* query_out, const void* query, const void* key, const void* value, int64_t query_stride,
               int64_t key_stride, int64_t value_stride, const void* q_norm_weight, const void* k_norm_weight, float eps,
@@ -307,6 +341,84 @@ int pkv_paged_attention_decode_step_int8(const void* new_keys, const void* new_v
                        num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, max_context_len,
                        partition_size, dtype, PKV_INT8, 1.f, 1.f, workspace, workspace_bytes, stream,
                        /*pdl=*/num_new_tokens > 0);
+}
+
+int pkv_paged_attention_prefill_chunk_int8(void* out, const void* query, const void* key_cache,
+                                           const void* value_cache, const int32_t* block_tables,
+                                           const int32_t* seq_lens, const int32_t* query_start_loc, int num_chunks,
+                                           int64_t total_q_tokens, int max_q_len, float scale, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                                           int64_t num_blocks, int dtype, pkv_stream_t stream) {
+    if (dtype != PKV_F16 && dtype != PKV_BF16) return PKV_EUNSUPPORTED;
+    if (num_chunks < 0 || total_q_tokens < 0 || max_q_len < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+        max_blocks_per_seq <= 0 || num_blocks <= 0 || !std::isfinite(scale))
+        return PKV_EINVAL;
+    if (num_q_heads % num_kv_heads) return PKV_EINVAL;
+    const int group = num_q_heads / num_kv_heads;
+    if (!supported_group(group) || (head_dim != 64 && head_dim != 128) ||
+        (block_size != 8 && block_size != 16 && block_size != 32))
+        return PKV_EUNSUPPORTED;
+    if (num_blocks >= (int64_t)INT32_MAX || (int64_t)max_blocks_per_seq * block_size > INT32_MAX ||
+        total_q_tokens > INT32_MAX)
+        return PKV_EINVAL;
+    if (num_chunks == 0 || total_q_tokens == 0 || max_q_len == 0) return PKV_OK;
+    if (!out || !query || !key_cache || !value_cache || !block_tables || !seq_lens || !query_start_loc)
+        return PKV_EINVAL;
+    if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache) ||
+        (reinterpret_cast<uintptr_t>(block_tables) & 3) || (reinterpret_cast<uintptr_t>(seq_lens) & 3) ||
+        (reinterpret_cast<uintptr_t>(query_start_loc) & 3))
+        return PKV_EINVAL;
+    const int tile_tokens = 128 / group;
+    const int64_t tile_pairs = ceil_div(ceil_div(max_q_len, tile_tokens), 2);
+    const int64_t grid = (int64_t)num_chunks * tile_pairs * num_kv_heads;
+    if (grid > INT32_MAX) return PKV_EUNSUPPORTED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (checked_mode()) {
+        std::vector<int32_t> qsl, lens;
+        int rc = fetch(qsl, query_start_loc, (size_t)num_chunks + 1, s);
+        if (rc) return rc;
+        rc = fetch(lens, seq_lens, (size_t)num_chunks, s);
+        if (rc) return rc;
+        if (qsl[0] < 0 || qsl[num_chunks] > total_q_tokens) return PKV_ERANGE;
+        for (int r = 0; r < num_chunks; ++r) {
+            const int n = qsl[r + 1] - qsl[r];
+            if (n < 0 || n > max_q_len || lens[r] < n) return PKV_ERANGE;
+        }
+        rc = check_tables(block_tables, seq_lens, num_chunks, max_blocks_per_seq, block_size, num_blocks,
+                          (int64_t)max_blocks_per_seq * block_size, s);
+        if (rc) return rc;
+    }
+    CUtensorMap tq, tk, tv;
+    int rc = make_query_map(&tq, query, dtype, total_q_tokens, num_q_heads, head_dim, group);
+    if (rc) return rc;
+    rc = make_int8_map(&tk, key_cache, num_blocks, block_size, num_kv_heads, head_dim);
+    if (rc) return rc;
+    rc = make_int8_map(&tv, value_cache, num_blocks, block_size, num_kv_heads, head_dim);
+    if (rc) return rc;
+    pkv::PrefillInt8Params prm;
+    prm.base.out = out;
+    prm.base.block_tables = block_tables;
+    prm.base.seq_lens = seq_lens;
+    prm.base.query_start_loc = query_start_loc;
+    prm.base.scale_log2 = scale * 1.4426950408889634f;
+    prm.base.out_scale = 1.f;
+    prm.base.num_chunks = num_chunks;
+    prm.base.num_q_heads = num_q_heads;
+    prm.base.num_kv_heads = num_kv_heads;
+    prm.base.max_blocks_per_seq = max_blocks_per_seq;
+    prm.base.block_size = block_size;
+    prm.base.num_blocks = num_blocks;
+    prm.base.tile_pairs = (int)tile_pairs;
+    const int64_t codes = (int64_t)block_size * num_kv_heads * head_dim;
+    prm.k_scales = static_cast<const uint8_t*>(key_cache) + codes;
+    prm.v_scales = static_cast<const uint8_t*>(value_cache) + codes;
+    prm.block_bytes = pkv::int8_block_bytes(block_size, num_kv_heads, head_dim);
+    const bool bf16 = dtype == PKV_BF16;
+    if (head_dim == 64)
+        return bf16 ? prefill_int8_by_group<__nv_bfloat16, 64>(group, prm, tq, tk, tv, (int)grid, s)
+                    : prefill_int8_by_group<__half, 64>(group, prm, tq, tk, tv, (int)grid, s);
+    return bf16 ? prefill_int8_by_group<__nv_bfloat16, 128>(group, prm, tq, tk, tv, (int)grid, s)
+                : prefill_int8_by_group<__half, 128>(group, prm, tq, tk, tv, (int)grid, s);
 }
 
 }  // extern "C"

@@ -25,6 +25,7 @@
 #include "decode_int8.cuh"
 #include "decode_multi.cuh"
 #include "prefill.cuh"
+#include "prefill_int8.cuh"
 
 namespace {
 

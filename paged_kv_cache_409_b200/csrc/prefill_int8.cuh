@@ -1,0 +1,515 @@
+// prefill_int8.cuh -- causal chunked-prefill attention over int8 pools on the
+// tcgen05 tensor cores: the pipeline of prefill.cuh (two query tiles of 128
+// rows per CTA, S and P in tensor memory, one softmax thread per row) with the
+// K and V tiles widened in shared memory by warps of their own, so that the
+// cache is read once, as it lies, and no scratch is needed.
+//
+// Widening.  Tile rows arrive as codes (16 KB at head_dim 128) with one fp32
+// scale each.  A converter thread turns four codes into two f16 pairs: a byte
+// permute puts 0x64 over each code (1024 + u), a subtraction of 1152 leaves
+// u - 128 exactly, and scale * (u - 128) is formed as c * s_hi + c * s_lo with
+// the scale split in two f16 parts, so that what is rounded is the product
+// (2^-11 of the element; 2^-25 absolute below 2^-14), not the scale.  Rows past
+// the sequence and rows of bad blocks are written as zeros: P is zero there,
+// and 0 * NaN must not reach O.  For the same reason a V row whose scale is NaN
+// (or beyond f16) becomes zeros and its K row NaN: the scores that see the row
+// are NaN, those that the causal mask hides stay out of it.
+//
+// Roles (512 threads; the registers of the second half go to the softmax):
+//   warps 0-7   softmax, four per query tile, as in prefill.cuh; with bf16
+//               queries they first turn the two Q tiles into f16 in place
+//   warp 8      loader: Q tiles, then the codes and scales of K_j and V_j into
+//               one staging buffer each, refilled when it has been widened
+//   warp 9      MMA issue
+//   warps 12-15 converters: staging -> f16 K (two stages) and V (two stages)
+// Every wait is bounded, as in prefill.cuh.
+#pragma once
+
+#include "decode_int8.cuh"
+#include "prefill.cuh"
+
+namespace pkv {
+
+struct PrefillInt8Params {
+    PrefillParams base;
+    const uint8_t* k_scales;  // scales of block 0
+    const uint8_t* v_scales;
+    int64_t block_bytes;
+};
+
+constexpr int kPrefillInt8Threads = 512;
+constexpr int kPrefillInt8ConvWarp = 12;   // first of four
+constexpr int kPrefillInt8ConvThreads = 128;
+
+template <int D, int G>
+struct PrefillInt8Cfg {
+    static constexpr int BM = 128, TT = BM / G, BN = 128;
+    static constexpr int NP = D / 64;               // 128-byte panels per f16 row
+    static constexpr int Q_BYTES = NP * BM * 128;   // one query tile
+    static constexpr int KT_BYTES = NP * BN * 128;  // one f16 K (or V) tile
+    static constexpr int C_BYTES = BN * D;          // the codes of a tile
+    static constexpr int Q_OFF = 0;
+    static constexpr int K_OFF = Q_OFF + 2 * Q_BYTES;    // [2] stages
+    static constexpr int V_OFF = K_OFF + 2 * KT_BYTES;   // [2] stages
+    static constexpr int KC_OFF = V_OFF + 2 * KT_BYTES;  // staging of K, then of V
+    static constexpr int VC_OFF = KC_OFF + C_BYTES;
+    static constexpr int SC_OFF = VC_OFF + C_BYTES;      // scales: K [BN], V [2][BN] (tile j in j & 1)
+    static constexpr int BAR_OFF = SC_OFF + 3 * BN * 4;
+    static constexpr int NBAR = 26;
+    static constexpr int SMEM = 1024 + BAR_OFF + NBAR * 8;
+    static constexpr uint32_t TMEM_COLS = 512, S_COL0 = 0, O_COL0 = 256;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+
+__device__ __forceinline__ uint32_t hmul2_u(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
+__device__ __forceinline__ uint32_t hfma2_u(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t y;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
+    return y;
+}
+
+// Four codes (one 32-bit word) times a scale split in two f16 parts.
+__device__ __forceinline__ uint2 widen_codes4(uint32_t u, uint32_t s_hi, uint32_t s_lo) {
+    const uint32_t a = hsub2_1152(__byte_perm(u, 0x64646464u, 0x4140));
+    const uint32_t b = hsub2_1152(__byte_perm(u, 0x64646464u, 0x4342));
+    return make_uint2(hfma2_u(a, s_hi, hmul2_u(a, s_lo)), hfma2_u(b, s_hi, hmul2_u(b, s_lo)));
+}
+
+// T: the query's and output's type; the MMAs run in f16.
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kPrefillInt8Threads, 1)
+    paged_prefill_int8_kernel(const PrefillInt8Params prm, const __grid_constant__ CUtensorMap tm_q,
+                              const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+    using C = PrefillInt8Cfg<D, G>;
+    const PrefillParams& p = prm.base;
+    const int B = p.block_size;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align_1024(smem_raw);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+    constexpr bool kNarrowQ = Elem<T>::kCuType == CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    uint64_t* q_full = bars + 0;
+    uint64_t* q_ready = bars + 1;   // Q tiles in f16 (256 arrivals; bf16 queries)
+    uint64_t* c_full = bars + 2;    // [2] codes of K and both scales | codes of V landed
+    uint64_t* c_free = bars + 4;    // [2] widened (128 arrivals)
+    uint64_t* k_full = bars + 6;    // [2] f16 K tile written (128 arrivals)
+    uint64_t* k_free = bars + 8;    // [2] the S MMAs that read the stage are done
+    uint64_t* v_full = bars + 10;   // [2]
+    uint64_t* v_free = bars + 12;   // [2]
+    uint64_t* s_full = bars + 14;   // [2] per tile: S_x(j) done
+    uint64_t* p_full = bars + 16;   // [2] per tile: P_x(j) written (128 arrivals)
+    uint64_t* o_full = bars + 18;   // [2] per tile: the tile's last P.V done
+    uint64_t* mma_done = bars + 20;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 22);
+
+    const int g = static_cast<int>(blockIdx.x) % p.num_kv_heads;
+    const int item = static_cast<int>(blockIdx.x) / p.num_kv_heads;
+    int r, pair;
+    if (p.num_chunks <= kLptChunks) {
+        if (!prefill_item(p.seq_lens, p.query_start_loc, p.num_chunks, C::TT, p.tile_pairs, item, r, pair)) return;
+    } else {
+        pair = p.tile_pairs - 1 - item / p.num_chunks;
+        r = item % p.num_chunks;
+    }
+    const int tid = threadIdx.x;
+    const int warp = tid >> 5;
+
+    const int q0 = p.query_start_loc[r];
+    const int n = p.query_start_loc[r + 1] - q0;
+    const int L = p.seq_lens[r];
+    const int c0 = L - n;
+    if (n < 0 || c0 < 0 || L > p.max_blocks_per_seq * B || n > 2 * p.tile_pairs * C::TT) {
+        if (tid == 0 && pair == 0 && g == 0) flag_error(PKV_DEVERR_LENGTH);
+        if (n < 0 || c0 < 0 || L > p.max_blocks_per_seq * B) return;
+    }
+    const int qt0 = 2 * pair;
+    if (qt0 * C::TT >= n) return;
+    const bool has_b = (qt0 + 1) * C::TT < n;
+    const int nkt_a = (c0 + min((qt0 + 1) * C::TT, n) - 1) / C::BN + 1;
+    const int nkt_b = has_b ? (c0 + min((qt0 + 2) * C::TT, n) - 1) / C::BN + 1 : 0;
+    const int nkt = max(nkt_a, nkt_b);
+    const int nblk = (L + B - 1) / B;
+    const int32_t* bt_row = p.block_tables + static_cast<int64_t>(r) * p.max_blocks_per_seq;
+
+    if (warp == 0) {
+        tmem_alloc(tmem_slot, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_ready, 256);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c_full[i], 1);
+            mbar_init(&c_free[i], kPrefillInt8ConvThreads);
+            mbar_init(&k_full[i], kPrefillInt8ConvThreads);
+            mbar_init(&v_full[i], kPrefillInt8ConvThreads);
+            mbar_init(&k_free[i], 1);
+            mbar_init(&v_free[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 128);
+            mbar_init(&o_full[i], 1);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    // 512 threads launch with 128 registers each; half of them hand 80 of
+    // theirs to the softmax threads, which hold a row of 128 scores:
+    // 256 * 208 + 256 * 48 = 512 * 128.
+    if (warp >= 8) {
+        regs_dec<48>();
+        if (warp == kPrefillLoadWarp) {
+            // ============================================================ loader (whole warp, lane 0 issues)
+            const int lane = tid & 31;
+            const bool leader = lane == 0;
+            const int per_tile = C::BN / B;  // blocks per key tile (4..16)
+            float* scales = reinterpret_cast<float*>(smem + C::SC_OFF);
+            auto fetch_ids = [&](int j) -> int {
+                const int lb = j * per_tile + lane;
+                return (lane < per_tile && lb < nblk) ? bt_row[lb] : -1;
+            };
+            // The codes of tile j, K (which = 0, with the tile's K and V scales) or
+            // V.  Rows of blocks that are not loaded get the scale 0: zeros.
+            auto load_codes = [&](int which, const CUtensorMap* map, int j, int ids) {
+                uint8_t* dst = smem + (which ? C::VC_OFF : C::KC_OFF);
+                float* ks = scales;
+                float* vs = scales + (1 + (j & 1)) * C::BN;
+                if (which == 0 && lane < per_tile && ids < 0)
+                    for (int i = 0; i < B; ++i) ks[lane * B + i] = vs[lane * B + i] = 0.f;
+                const unsigned good = __ballot_sync(0xffffffffu, lane < per_tile && ids >= 0);
+                if (leader) {
+                    fence_proxy_async();  // the converters' reads before the next copies
+                    mbar_arrive_expect_tx(&c_full[which], C::C_BYTES + (which ? 0 : __popc(good) * 2 * B * 4));
+                }
+                for (int i = 0; i < per_tile; ++i) {
+                    const int id = __shfl_sync(0xffffffffu, ids, i);
+                    if (!leader) continue;
+                    const int coord = id >= 0 ? id : static_cast<int>(p.num_blocks);  // out of range: zero fill
+                    tma_load_4d(dst + i * B * D, map, 0, g, 0, coord, &c_full[which]);
+                    if (which == 0 && id >= 0) {
+                        const int64_t off = id * prm.block_bytes + g * (B * 4);
+                        bulk_load(ks + i * B, prm.k_scales + off, B * 4, &c_full[0]);
+                        bulk_load(vs + i * B, prm.v_scales + off, B * 4, &c_full[0]);
+                    }
+                }
+            };
+            if (leader) {
+                mbar_arrive_expect_tx(q_full, (has_b ? 2 : 1) * C::Q_BYTES);
+                for (int x = 0; x < (has_b ? 2 : 1); ++x) {
+#pragma unroll
+                    for (int pn = 0; pn < C::NP; ++pn)
+                        tma_load_3d(smem + C::Q_OFF + x * C::Q_BYTES + pn * C::BM * 128, &tm_q, pn * 64, g * G,
+                                    q0 + (qt0 + x) * C::TT, q_full);
+                }
+            }
+            int ids = fetch_ids(0);
+            int loaded_k = 0, loaded_v = 0;
+            for (int j = 0; j < nkt; ++j) {
+                const int ids_next = fetch_ids(j + 1);
+                if (lane < per_tile && j * per_tile + lane < nblk && (ids < 0 || ids >= p.num_blocks)) {
+                    flag_error(PKV_DEVERR_BLOCK_ID);
+                    ids = -1;
+                }
+                if (j > 0 && !__all_sync(0xffffffffu, mbar_wait_or_abort_idle(&c_free[0], (j - 1) & 1, abort_flag))) break;
+                load_codes(0, &tm_k, j, ids);
+                loaded_k = j + 1;
+                if (j > 0 && !__all_sync(0xffffffffu, mbar_wait_or_abort_idle(&c_free[1], (j - 1) & 1, abort_flag))) break;
+                load_codes(1, &tm_v, j, ids);
+                loaded_v = j + 1;
+                ids = ids_next;
+            }
+            if (leader) {
+                // wait (bounded) for this warp's last copies before the CTA may exit
+                mbar_wait(q_full, 0);
+                if (loaded_k > 0) mbar_wait(&c_full[0], (loaded_k - 1) & 1);
+                if (loaded_v > 0) mbar_wait(&c_full[1], (loaded_v - 1) & 1);
+            }
+        } else if (warp == kPrefillMmaWarp) {
+            // ============================================================ MMA issue (lane 0)
+            if ((tid & 31) == 0) {
+                constexpr uint32_t IDESC_S = umma_idesc_f16(128, C::BN, false, false, false);
+                constexpr uint32_t IDESC_O = umma_idesc_f16(128, D, false, false, true);
+                uint64_t qdesc[2], kdesc[2], vdesc[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    qdesc[i] = smem_desc_sw128(smem_u32(smem + C::Q_OFF + i * C::Q_BYTES), 16, 1024);
+                    kdesc[i] = smem_desc_sw128(smem_u32(smem + C::K_OFF + i * C::KT_BYTES), 16, 1024);
+                    vdesc[i] = smem_desc_sw128(smem_u32(smem + C::V_OFF + i * C::KT_BYTES), C::BN * 128, 1024);
+                }
+                auto issue_s = [&](int x, int t) {  // S_x(t) = Q_x . K_t^T
+                    const uint64_t qd = x ? qdesc[1] : qdesc[0], kd = (t & 1) ? kdesc[1] : kdesc[0];
+                    const uint32_t s_col = C::S_COL0 + 128 * x;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        constexpr int kQ = C::BM * 128 / 16, kK = C::BN * 128 / 16;  // panel strides / 16
+                        umma_f16_ss(tmem + s_col, qd + (kk / 4) * kQ + (kk % 4) * 2, kd + (kk / 4) * kK + (kk % 4) * 2,
+                                    IDESC_S, kk > 0);
+                    }
+                    umma_commit(&s_full[x]);
+                };
+                auto issue_pv = [&](int x, int t, bool last) {  // O_x += P_x(t) . V_t, P from tensor memory
+                    const uint64_t vd = (t & 1) ? vdesc[1] : vdesc[0];
+                    const uint32_t p_col = C::S_COL0 + 128 * x, o_col = C::O_COL0 + D * x;
+#pragma unroll
+                    for (int kk = 0; kk < C::BN / 16; ++kk)
+                        umma_f16_ts(tmem + o_col, tmem + p_col + kk * 8, vd + kk * (16 * 128 / 16), IDESC_O,
+                                    t > 0 || kk > 0);
+                    if (last) umma_commit(&o_full[x]);
+                };
+                bool ok = mbar_wait_or_abort(kNarrowQ ? q_ready : q_full, 0, abort_flag) &&
+                          mbar_wait_or_abort(&k_full[0], 0, abort_flag);
+                if (ok) {
+                    tc_fence_after();
+                    issue_s(0, 0);
+                    if (nkt_b > 0) issue_s(1, 0);
+                    umma_commit(&k_free[0]);
+                }
+                for (int t = 0; ok && t < nkt; ++t) {
+                    const bool next = t + 1 < nkt;
+                    bool k_next = false;
+                    ok = mbar_wait_or_abort(&v_full[t & 1], (t >> 1) & 1, abort_flag);
+                    for (int x = 0; ok && x < 2; ++x) {
+                        const int nk = x == 0 ? nkt_a : nkt_b;
+                        if (t >= nk) continue;
+                        ok = mbar_wait_or_abort(&p_full[x], t & 1, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_pv(x, t, t + 1 == nk);
+                        if (t + 1 < nk) {
+                            if (!k_next) {
+                                ok = k_next = mbar_wait_or_abort(&k_full[(t + 1) & 1], ((t + 1) >> 1) & 1, abort_flag);
+                                if (!ok) break;
+                                tc_fence_after();
+                            }
+                            issue_s(x, t + 1);
+                        }
+                    }
+                    if (ok) {
+                        umma_commit(&v_free[t & 1]);
+                        if (next) umma_commit(&k_free[(t + 1) & 1]);
+                    }
+                }
+                umma_commit(mma_done);  // every MMA done before tensor memory is released
+                mbar_wait(mma_done, 0);
+            }
+        } else if (warp >= kPrefillInt8ConvWarp) {
+            // ============================================================ converters
+            const int ct = tid - kPrefillInt8ConvWarp * 32;
+            const float* scales = reinterpret_cast<const float*>(smem + C::SC_OFF);
+            // Widen the staged codes of key tile j into an f16 tile: 16 codes
+            // (two 16-byte vectors of f16) per step.  Row r of the code tile is
+            // swizzled over D bytes, the f16 tile is D / 64 panels of 128-byte
+            // rows, swizzled over 128 bytes.
+            constexpr float kMaxScale = 65504.f / 128.f;
+            auto widen = [&](int which, int j, uint8_t* dst) {
+                const uint8_t* src = smem + (which ? C::VC_OFF : C::KC_OFF);
+                constexpr int VR = D / 16;  // 16-code vectors per row
+#pragma unroll 4
+                for (int e = ct; e < C::BN * VR; e += kPrefillInt8ConvThreads) {
+                    const int row = e / VR, ch = e % VR;
+                    const uint4 u = *reinterpret_cast<const uint4*>(src + int8_chunk<D>(row, ch));
+                    float s = scales[(which ? 1 + (j & 1) : 0) * C::BN + row];
+                    if (which) {
+                        if (!(s <= kMaxScale)) s = 0.f;
+                    } else if (!(scales[(1 + (j & 1)) * C::BN + row] <= kMaxScale) || !(s <= kMaxScale)) {
+                        s = __uint_as_float(0x7fc00000u);
+                    }
+                    if (j * C::BN + row >= L) s = 0.f;
+                    const __half hi = __float2half_rn(s);
+                    const __half lo = __float2half_rn(s - __half2float(hi));
+                    const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(lo);
+                    const uint32_t sh = *reinterpret_cast<const uint32_t*>(&hi2);
+                    const uint32_t sl = *reinterpret_cast<const uint32_t*>(&lo2);
+                    const uint2 a = widen_codes4(u.x, sh, sl), b = widen_codes4(u.y, sh, sl);
+                    const uint2 c = widen_codes4(u.z, sh, sl), d = widen_codes4(u.w, sh, sl);
+                    uint8_t* panel = dst + (ch / 4) * C::BN * 128 + row * 128;
+                    const int v0 = 2 * (ch % 4), sw = row & 7;
+                    *reinterpret_cast<uint4*>(panel + ((v0 ^ sw) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+                    *reinterpret_cast<uint4*>(panel + (((v0 + 1) ^ sw) << 4)) = make_uint4(c.x, c.y, d.x, d.y);
+                }
+                fence_proxy_async();  // the f16 tile -> the tensor cores' (async) proxy
+            };
+            for (int j = 0; j < nkt; ++j) {
+                const int st = j & 1;
+                if (!__all_sync(0xffffffffu, mbar_wait_or_abort_idle(&c_full[0], j & 1, abort_flag))) break;
+                if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait_or_abort_idle(&k_free[st], ((j - 2) >> 1) & 1, abort_flag)))
+                    break;
+                widen(0, j, smem + C::K_OFF + st * C::KT_BYTES);
+                mbar_arrive(&c_free[0]);
+                mbar_arrive(&k_full[st]);
+                if (!__all_sync(0xffffffffu, mbar_wait_or_abort_idle(&c_full[1], j & 1, abort_flag))) break;
+                if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait_or_abort_idle(&v_free[st], ((j - 2) >> 1) & 1, abort_flag)))
+                    break;
+                widen(1, j, smem + C::V_OFF + st * C::KT_BYTES);
+                mbar_arrive(&c_free[1]);
+                mbar_arrive(&v_full[st]);
+            }
+        }
+    } else {
+        regs_inc<208>();
+        // ================================================================ softmax: one thread per row
+        const int x = warp >> 2;
+        const int row = (warp & 3) * 32 + (tid & 31);
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const int tok = (qt0 + x) * C::TT + row / G;
+        const int qpos = c0 + tok;
+        const int nk = x == 0 ? nkt_a : nkt_b;
+        const uint32_t ts = tmem + lane_base + C::S_COL0 + 128 * x;
+        const uint32_t to = tmem + lane_base + C::O_COL0 + D * x;
+        const float sl2 = p.scale_log2;
+        constexpr float kRescaleLog2 = 8.f;
+        float m_used = -INFINITY, lsum = 0.f;
+        bool ok = true;
+        if constexpr (kNarrowQ) {  // this warpgroup's Q tile to f16, in place
+            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(q_full, 0, abort_flag));
+            if (ok) {
+                if (x == 0 || has_b) {
+                    uint8_t* q = smem + C::Q_OFF + x * C::Q_BYTES;
+#pragma unroll 4
+                    for (int off = row * 16; off < C::Q_BYTES; off += 128 * 16) {
+                        uint4 v = *reinterpret_cast<const uint4*>(q + off);
+                        auto narrow = [](uint32_t u) {
+                            const float2 f = Elem<__nv_bfloat16>::pair(u);
+                            return pack_half2(f.x, f.y);
+                        };
+                        v = make_uint4(narrow(v.x), narrow(v.y), narrow(v.z), narrow(v.w));
+                        *reinterpret_cast<uint4*>(q + off) = v;
+                    }
+                    fence_proxy_async();
+                }
+                mbar_arrive(q_ready);
+            }
+        }
+        for (int j = 0; ok && j < nk; ++j) {
+            if (!__all_sync(0xffffffffu, mbar_wait_or_abort(&s_full[x], j & 1, abort_flag))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            float sv[C::BN];
+            {
+                uint32_t u[C::BN];
+#pragma unroll
+                for (int c = 0; c < C::BN / 32; ++c)
+                    tmem_ld32_nowait(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]));
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < C::BN; ++i) sv[i] = __uint_as_float(u[i]);
+            }
+            const int k0 = j * C::BN;
+            const bool all_vis = k0 + C::BN - 1 <= qpos;
+            float mrow;
+            if (all_vis) {
+                float r0 = sv[0], r1 = sv[1], r2 = sv[2], r3 = sv[3];
+                if (sl2 >= 0.f) {
+#pragma unroll
+                    for (int i = 4; i < C::BN - 4; i += 8)
+                        r0 = fmax3(r0, sv[i], sv[i + 4]), r1 = fmax3(r1, sv[i + 1], sv[i + 5]),
+                        r2 = fmax3(r2, sv[i + 2], sv[i + 6]), r3 = fmax3(r3, sv[i + 3], sv[i + 7]);
+                    r0 = fmax3(r0, sv[C::BN - 4], sv[C::BN - 3]), r1 = fmax3(r1, sv[C::BN - 2], sv[C::BN - 1]);
+                    mrow = fmaxf(fmaxf(r0, r1), fmaxf(r2, r3)) * sl2;
+                } else {
+#pragma unroll
+                    for (int i = 4; i < C::BN - 4; i += 8)
+                        r0 = fmin3(r0, sv[i], sv[i + 4]), r1 = fmin3(r1, sv[i + 1], sv[i + 5]),
+                        r2 = fmin3(r2, sv[i + 2], sv[i + 6]), r3 = fmin3(r3, sv[i + 3], sv[i + 7]);
+                    r0 = fmin3(r0, sv[C::BN - 4], sv[C::BN - 3]), r1 = fmin3(r1, sv[C::BN - 2], sv[C::BN - 1]);
+                    mrow = fminf(fminf(r0, r1), fminf(r2, r3)) * sl2;
+                }
+            } else {
+                float r0 = -INFINITY, r1 = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < C::BN; i += 2) {
+                    sv[i] = k0 + i <= qpos ? sv[i] * sl2 : -INFINITY;
+                    sv[i + 1] = k0 + i + 1 <= qpos ? sv[i + 1] * sl2 : -INFINITY;
+                    r0 = fmaxf(r0, sv[i]);
+                    r1 = fmaxf(r1, sv[i + 1]);
+                }
+                mrow = fmaxf(r0, r1);
+            }
+            const bool rescale = mrow > m_used + kRescaleLog2 || (m_used == -INFINITY && mrow != -INFINITY);
+            float alpha = 1.f;
+            if (rescale) {
+                alpha = ex2_approx(m_used - mrow);  // 0 when m_used is -inf
+                m_used = mrow;
+            }
+            const float mexp = m_used == -INFINITY ? 0.f : m_used;
+            const float smul = all_vis ? sl2 : 1.f;
+            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 smul2 = make_float2(smul, smul), nm2 = make_float2(-mexp, -mexp);
+#pragma unroll
+            for (int c = 0; c < C::BN / 32; ++c) {
+                uint32_t pw[16];
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 arg = __ffma2_rn(make_float2(sv[c * 32 + i], sv[c * 32 + i + 1]), smul2, nm2);
+                    const float p0 = ex2_approx(arg.x), p1 = ex2_approx(arg.y);
+                    acc[(i / 2) & 1] = __fadd2_rn(acc[(i / 2) & 1], make_float2(p0, p1));
+                    pw[i / 2] = pack_half2(p0, p1);
+                }
+                tmem_st16_nowait(ts + c * 16, pw);
+            }
+            lsum = lsum * alpha + ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y));
+            if (j >= 1 && __any_sync(0xffffffffu, rescale && alpha != 1.f)) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    float v[32];
+                    tmem_ld32(to + c * 32, v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] *= alpha;
+                    tmem_st32(to + c * 32, v);
+                }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_full[x]);
+        }
+        if (ok && nk > 0) {
+            if (__all_sync(0xffffffffu, mbar_wait_or_abort(&o_full[x], 0, abort_flag))) {
+                tc_fence_after();
+                const bool live = tok < n && !*abort_flag;
+                const float inv = 1.f / lsum;
+                T* dst = reinterpret_cast<T*>(p.out) +
+                         (static_cast<int64_t>(q0 + tok) * p.num_q_heads + static_cast<int64_t>(g) * G + row % G) * D;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    float v[32];
+                    tmem_ld32(to + c * 32, v);
+                    if (live) {
+#pragma unroll
+                        for (int d = 0; d < 32; d += 8) {
+                            uint4 w;
+                            w.x = Elem<T>::pack(v[d] * inv, v[d + 1] * inv);
+                            w.y = Elem<T>::pack(v[d + 2] * inv, v[d + 3] * inv);
+                            w.z = Elem<T>::pack(v[d + 4] * inv, v[d + 5] * inv);
+                            w.w = Elem<T>::pack(v[d + 6] * inv, v[d + 7] * inv);
+                            *reinterpret_cast<uint4*>(dst + c * 32 + d) = w;
+                        }
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+}  // namespace pkv

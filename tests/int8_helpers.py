@@ -45,42 +45,44 @@ def rows_of(pool, table, n):
     return (codes[ids, pos % B].double() - 128) * s[..., None], s
 
 
-def reference(q, kp, vp, table, n, scale, dtype, first=None, query_error=True, value_error=0.0):
+def reference(q, kp, vp, table, n, scale, dtype, first=None):
     """Attention of the rows q [r, Hq, D] over the first n cached rows (row i over first[i] + 1 of them when `first`
-    is given), in 64 bits, and the error bound of each element of a result rounded to `dtype`.
+    is given: a chunk), in 64 bits, and the error bound of each element of a result rounded to `dtype`.
 
-    The query's 16-bit integer row is off by at most 0.52 steps of max |q| / 32639 an element (half a step, and
-    fp32's product), or, without query_error, by f16's half step: the scores by that times the key's sum of
-    magnitudes.  Scores, exponentials and sums in fp32, and the hardware's base-2 functions: 2e-5 of a weight at the
-    sizes used here (scores below 64 in log2 units: 4 roundings of 2^-24 each, 2^-22 for the functions).  A weight
-    goes into the product as f16: half a step, 2^-11, of it, or 2^-25 of the largest product of weight and V scale
-    (the base) for the small ones, times codes up to 127.  `value_error`: what the values themselves are rounded by,
-    relative."""
-    r, Hq, D = q.shape
+    Decode: the query's 16-bit integer row is off by at most 0.52 steps of max |q| / 32639 an element (half a step,
+    and fp32's product), a score by that times the key's sum of magnitudes.  Chunks: keys and values are widened to
+    f16, off by half a step, 2^-11 (2^-25 below 2^-14), and the scale's second part, under 2^-20.
+    Scores, exponentials and sums in fp32, and the hardware's base-2 functions: 2e-5 of a weight at the sizes used
+    here (scores below 64 in log2 units: 4 roundings of 2^-24 each, 2^-22 for the functions).  A weight goes into
+    the product as f16: half a step, 2^-11, of it, or 2^-25 of the base for the small ones; the base is at most the
+    largest product of weight and V scale (decode; then times codes up to 127) or weight (chunks)."""
     K, _ = rows_of(kp, table, n)
     V, vs = rows_of(vp, table, n)
-    G = Hq // K.shape[1]
+    G = q.shape[1] // K.shape[1]
     K, V, vs = (t.repeat_interleave(G, 1) for t in (K, V, vs))
     q = q.double()
     t = torch.einsum("rhd,nhd->rhn", q, K) * scale
     if first is not None:
-        j = torch.arange(n, device=q.device)
-        t = t.masked_fill(j[None, None, :] > first[:, None, None], -float("inf"))
+        hidden = torch.arange(n, device=q.device)[None, None, :] > first[:, None, None]
+        t = t.masked_fill(hidden, -float("inf"))
     p = torch.softmax(t, -1)
     ref = torch.einsum("rhn,nhd->rhd", p, V)
     size = torch.einsum("rhn,nhd->rhd", p, V.abs())
-    if query_error:
-        dq = 0.52 * q.abs().amax(-1) / 32639
-        ds = abs(scale) * dq * K.abs().sum(-1).amax(0)
+    tiny = 2.0 ** -25 if dtype == torch.float16 else 0.0
+    if first is None:
+        ds = abs(scale) * 0.52 * q.abs().amax(-1) / 32639 * K.abs().sum(-1).amax(0)
+        weight, top = 2.0 ** -11, (p * vs.T[None]).amax(-1) * 127
     else:
-        ds = abs(scale) * torch.einsum("rhd,nhd->rhn", q.abs(), K.abs()).amax(-1) * 2.0 ** -10
-    top = (p * vs.T[None]).amax(-1) * 127
-    bound = torch.finfo(dtype).eps / 2 * ref.abs() * (1 + 2.0 ** -10) + (2.0 ** -11 + 2e-5 + value_error + 2 * ds)[..., None] * size \
-        + (n * 2.0 ** -25 * top)[..., None] + (2.0 ** -25 if dtype == torch.float16 else 0.0)
+        ds = abs(scale) * ((2.0 ** -11 + 2.0 ** -20) * torch.einsum("rhd,nhd->rhn", q.abs(), K.abs()).amax(-1)
+                           + 2.0 ** -25 * q.abs().sum(-1))
+        weight, top = 2.0 ** -10 + 2.0 ** -20, p.amax(-1) * V.abs().amax()
+        tiny += 2.0 ** -25
+    bound = torch.finfo(dtype).eps / 2 * ref.abs() * (1 + 2.0 ** -10) + (weight + 2e-5 + 2 * ds)[..., None] * size \
+        + (n * 2.0 ** -25 * top)[..., None] + tiny
     return ref, bound
 
 
 def check(out, ref, bound, what=""):
     assert bool(torch.isfinite(out.double()).all()), f"{what}: non-finite"
     over = (out.double() - ref).abs() - bound
-    assert float(over.max()) <= 0 if over.numel() else True, f"{what}: over by {float(over.max())}"
+    assert over.numel() == 0 or float(over.max()) <= 0, f"{what}: over by {float(over.max())}"

@@ -1,0 +1,209 @@
+"""Chunked prefill over int8 pools against plain 64-bit attention over the same codes and scales, and a serving run
+of the row calls together: table, rotation and append, prefill, decode steps."""
+import pytest
+import torch
+
+import paged_kv_cache_409_b200 as pkv
+from int8_helpers import check, make_pools, reference
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def starts(ns):
+    return torch.tensor([0] + list(ns), device="cuda").cumsum(0).to(torch.int32)
+
+
+def run(q, kp, vp, bt, ns, lens, scale, max_n=None, out=None, **kw):
+    out = torch.full_like(q, 7.0) if out is None else out
+    return pkv.paged_attention_prefill_chunk_int8(out, q, kp, vp, bt, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                                  starts(ns), max_n or max(ns), scale, **kw)
+
+
+def verify(out, q, kp, vp, bt, ns, lens, scale, what="", only=None):
+    at = 0
+    for i, (n, L) in enumerate(zip(ns, lens)):
+        if n and (only is None or i in only):
+            first = torch.arange(L - n, L, device="cuda")
+            ref, bound = reference(q[at: at + n], kp, vp, bt[i], L, scale, q.dtype, first=first)
+            check(out[at: at + n], ref, bound, f"{what} chunk {i}")
+        at += n
+
+
+CASES = [
+    # dt, D, B, Hq, Hkv, cached before, new
+    ("bf16", 128, 32, 32, 8, [0, 300], [512, 77]),
+    ("f16", 128, 16, 8, 8, [5, 0, 129], [1, 130, 128]),
+    ("bf16", 64, 8, 16, 2, [1000, 0], [33, 257]),
+    ("f16", 64, 16, 4, 2, [17], [300]),
+    ("bf16", 128, 16, 16, 2, [255, 64], [200, 16]),
+    ("f16", 128, 8, 4, 1, [0, 127, 1, 0], [1, 1, 0, 2]),
+    ("bf16", 128, 32, 2, 2, [640], [384]),
+    ("f16", 64, 32, 8, 1, [4000, 3], [6, 5]),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=[f"case{i}" for i in range(len(CASES))])
+def test_prefill(case):
+    dt, D, B, Hq, Hkv, c0, ns = case
+    lens = [a + b for a, b in zip(c0, ns)]
+    kp, vp, bt = make_pools(lens, B, Hkv, D, seed=D + B)
+    q = torch.randn(sum(ns) + 3, Hq, D, device="cuda").to(DT[dt])  # three rows behind the last chunk
+    out = run(q, kp, vp, bt, ns, lens, D ** -0.5)
+    assert pkv.get_device_error() == 0
+    verify(out, q, kp, vp, bt, ns, lens, D ** -0.5)
+    assert bool((out[sum(ns):] == 7.0).all())
+
+
+def test_prefill_many_chunks():
+    """More chunks than the longest-first order takes (64), of different lengths, a bound above the longest."""
+    ns = [(5 * i) % 7 for i in range(70)]
+    lens = [n + (37 * i) % 300 for i, n in enumerate(ns)]
+    kp, vp, bt = make_pools(lens, 16, 2, 64, seed=1)
+    q = torch.randn(sum(ns), 4, 64, device="cuda").half()
+    out = run(q, kp, vp, bt, ns, lens, 0.125, max_n=200)
+    assert pkv.get_device_error() == 0
+    verify(out, q, kp, vp, bt, ns, lens, 0.125)
+
+
+@pytest.mark.parametrize("kw", [dict(v_size=1e-3), dict(v_size=200.0), dict(k_size=6.0), dict(v_spread=5)], ids=str)
+def test_prefill_row_scales(kw):
+    ns, lens = [140, 9], [333, 9]
+    kp, vp, bt = make_pools(lens, 8, 2, 128, seed=2, **kw)
+    q = torch.randn(149, 8, 128, device="cuda").bfloat16()
+    for scale in (0.088, -0.05, 0.0):
+        verify(run(q, kp, vp, bt, ns, lens, scale), q, kp, vp, bt, ns, lens, scale, str(kw))
+
+
+def test_prefill_nan_rows_show_where_they_are_seen():
+    """A K or V row of scale NaN, or beyond f16, reaches the rows at or behind its position and no other; a NaN query
+    row reaches itself."""
+    ns, lens = [150, 40], [190, 90]
+    kp, vp, bt = make_pools(lens, 16, 2, 64, seed=3)
+    q = torch.randn(190, 4, 64, device="cuda").bfloat16()
+    ref = run(q, kp, vp, bt, ns, lens, 0.1)
+    good = torch.ones(1, 2, 64, device="cuda")
+    slot = (bt[0, 5].long() * 16 + 4).view(1)  # position 84: row 44 of chunk 0
+    for bad in (torch.full_like(good, float("nan")), torch.full_like(good, 1e6)):
+        for which in (0, 1):
+            k2, v2 = kp.clone(), vp.clone()
+            pkv.reshape_and_cache_int8(bad if which == 0 else good, bad if which == 1 else good, k2, v2, slot)
+            out = run(q, k2, v2, bt, ns, lens, 0.1)
+            assert bool(torch.isnan(out[44:150]).all())
+            assert torch.equal(out[:44], ref[:44]) and torch.equal(out[150:], ref[150:])
+    q[160, 1, 3] = float("nan")
+    out = run(q, kp, vp, bt, ns, lens, 0.1)
+    nan = torch.zeros(190, 4, dtype=torch.bool, device="cuda")
+    nan[160, 1] = True
+    assert torch.equal(torch.isnan(out).all(-1), nan) and torch.equal(torch.isnan(out).any(-1), nan)
+    assert torch.equal(out[~nan], ref[~nan])
+
+
+def test_prefill_bad_tables_are_flagged():
+    ns, lens = [64, 30, 50], [200, 30, 180]
+    kp, vp, bt = make_pools(lens, 16, 2, 128, seed=4)
+    q = torch.randn(144, 4, 128, device="cuda").half()
+    ref = run(q, kp, vp, bt, ns, lens, 0.1)
+    assert pkv.get_device_error() == 0
+    for col, bad in ((0, -1), (7, kp.shape[0]), (12, 1 << 30)):
+        t = bt.clone()
+        t[0, col] = bad
+        out = run(q, kp, vp, t, ns, lens, 0.1)
+        assert pkv.get_device_error() == pkv._binding.DEVERR_BLOCK_ID
+        assert torch.equal(out[64:], ref[64:])
+    for wrong in ([200, 20, 180], [200, 30, bt.shape[1] * 16 + 1]):  # shorter than its chunk; beyond the table
+        out = run(q, kp, vp, bt, ns, wrong, 0.1)
+        assert pkv.get_device_error() == pkv._binding.DEVERR_LENGTH
+        assert torch.equal(out[:64], ref[:64])
+
+
+def test_prefill_row_of_one_equals_decode_closely_and_repeats():
+    """Chunks of one row are decode; the same call twice gives the same bits, on two streams at once too."""
+    lens = [513, 100, 1]
+    kp, vp, bt = make_pools(lens, 32, 2, 128, seed=5)
+    q = torch.randn(3, 16, 128, device="cuda").half()
+    a = run(q, kp, vp, bt, [1, 1, 1], lens, 0.09)
+    verify(a, q, kp, vp, bt, [1, 1, 1], lens, 0.09)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(4):
+        for st in streams:
+            with torch.cuda.stream(st):
+                outs.append(run(q, kp, vp, bt, [1, 1, 1], lens, 0.09))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, a) for o in outs)
+
+
+def test_prefill_wait_limit():
+    ns, lens = [256] * 4, [4096] * 4
+    kp, vp, bt = make_pools(lens, 16, 2, 128, seed=6)
+    q = torch.randn(1024, 8, 128, device="cuda").bfloat16()
+    pkv.set_wait_limit_ns(0)
+    try:
+        run(q, kp, vp, bt, ns, lens, 0.1)
+        torch.cuda.synchronize()
+        assert pkv.get_device_error() & pkv._binding.DEVERR_TIMEOUT
+    finally:
+        pkv.set_wait_limit_ns(pkv.DEFAULT_WAIT_LIMIT_NS)
+    out = run(q, kp, vp, bt, ns, lens, 0.1)
+    assert pkv.get_device_error() == 0
+    verify(out, q, kp, vp, bt, ns, lens, 0.1, only=[0, 3])
+
+
+def test_serving_run():
+    """Two sequences through one layer: rotary table, chunked prompts (rotation and append, then prefill), and decode
+    steps in a captured graph, against 64-bit attention over the rows as they were rotated and quantised."""
+    B, Hq, Hkv, D, R = 16, 8, 2, 128, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    table = torch.empty(2048, R, device="cuda")
+    pkv.rope_table(table, base=10000.0, scaling="by_parts", factor=4.0, original_max_position=512, beta=8.0)
+    NB = 64
+    perm = torch.randperm(NB, device="cuda", generator=g).to(torch.int32)
+    bt = perm.view(2, 32).contiguous()
+    kp, vp = (torch.zeros(NB, B, Hkv, D + 4, dtype=torch.uint8, device="cuda") for _ in range(2))
+    kw = dict(q_norm_weight=torch.ones(D, device="cuda").half(), k_norm_weight=torch.ones(D, device="cuda").half())
+    lens = [0, 0]
+
+    def project(n):
+        x = torch.randn(n, (Hq + 2 * Hkv) * D, device="cuda", generator=g).half()
+        return (x[:, : Hq * D].view(n, Hq, D), x[:, Hq * D: (Hq + Hkv) * D].view(n, Hkv, D),
+                x[:, (Hq + Hkv) * D:].view(n, Hkv, D))
+
+    for ns in ([130, 7], [60, 200]):
+        seq = torch.repeat_interleave(torch.arange(2, device="cuda"), torch.tensor(ns, device="cuda"))
+        pos = torch.cat([torch.arange(c, c + n, device="cuda") for c, n in zip(lens, ns)])
+        slots = bt[seq, pos // B].long() * B + pos % B
+        q, k, v = project(sum(ns))
+        qr = torch.empty(sum(ns), Hq, D, dtype=torch.half, device="cuda")
+        pkv.rope_and_cache_int8(qr, q, k, v, table, pos, kp, vp, slots, **kw)
+        lens = [c + n for c, n in zip(lens, ns)]
+        out = run(qr, kp, vp, bt, ns, lens, D ** -0.5)
+        verify(out, qr, kp, vp, bt, ns, lens, D ** -0.5)
+    q, k, v = (t.contiguous() for t in project(2))
+    qr, out = torch.empty_like(q), torch.empty_like(q)
+    pos = torch.tensor(lens, device="cuda")
+    slots, cl = torch.empty_like(pos), torch.empty(2, dtype=torch.int32, device="cuda")
+
+    def step():
+        slots.copy_(bt.gather(1, (pos // B)[:, None])[:, 0].long() * B + pos % B)
+        cl.copy_(pos + 1)
+        pkv.rope_and_cache_int8(qr, q, k, v, table, pos, kp, vp, slots, **kw)
+        pkv.paged_attention_decode_int8(out, qr, kp, vp, bt, cl, D ** -0.5, 512, partition_size=0)
+        pos.add_(1)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(20):
+        for t, new in zip((q, k, v), project(2)):
+            t.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, n in enumerate(pos.tolist()):
+            ref, bound = reference(qr[i: i + 1], kp, vp, bt[i], n, D ** -0.5, torch.half)
+            check(out[i: i + 1], ref, bound, f"step at {n}")
+    assert pkv.get_device_error() == 0

@@ -200,3 +200,45 @@ def test_decode_int8_refusals():
     assert dec(step, (P, P, P, 0), dt=0) == EUNSUPPORTED
     assert pkv.decode_partition_size(64, 32, 32, 128, 16, 2048, pkv.INT8) == 0
     assert lib.pkv_paged_attention_decode(P, P, P, P, P, P, 0.1, 1, 4, 2, 64, 16, 4, 8, 64, 0, 4, None, 0, None) == -2
+
+
+def test_prefill_int8_arguments_and_refusals(mock):  # noqa: F811
+    R, Tq, Hq, Hkv, D, B, NB, MB = 2, 9, 8, 2, 128, 16, 23, 6
+    q = torch.zeros(Tq, Hq, D, dtype=torch.float16)
+    out = torch.zeros_like(q)
+    kc, vc = (torch.zeros(NB, B, Hkv, D + 4, dtype=torch.uint8) for _ in range(2))
+    bt, sl = torch.zeros(R, MB, dtype=torch.int32), torch.zeros(R, dtype=torch.int32)
+    qsl = torch.zeros(R + 1, dtype=torch.int32)
+    pkv.paged_attention_prefill_chunk_int8(out, q, kc, vc, bt, sl, qsl, 5, 0.7, stream=4)
+    name, a = mock.last()
+    assert name == "pkv_paged_attention_prefill_chunk_int8"
+    assert a == {"out": out.data_ptr(), "query": q.data_ptr(), "key_cache": kc.data_ptr(), "value_cache": vc.data_ptr(),
+                 "block_tables": bt.data_ptr(), "seq_lens": sl.data_ptr(), "query_start_loc": qsl.data_ptr(),
+                 "num_chunks": R, "total_q_tokens": Tq, "max_q_len": 5, "scale": f32(0.7), "num_q_heads": Hq,
+                 "num_kv_heads": Hkv, "head_dim": D, "block_size": B, "max_blocks_per_seq": MB, "num_blocks": NB,
+                 "dtype": 1, "stream": 4}
+    for bad in (dict(query=q[:, :, :64]), dict(out=out.bfloat16()), dict(query_start_loc=qsl[:2]),
+                dict(block_tables=bt[:1]), dict(seq_lens=sl.long()), dict(value_cache=vc[:2])):
+        kw = dict(out=out, query=q, key_cache=kc, value_cache=vc, block_tables=bt, seq_lens=sl, query_start_loc=qsl)
+        with pytest.raises(ValueError):
+            pkv.paged_attention_prefill_chunk_int8(**{**kw, **bad}, max_q_len=5, scale=0.7)
+
+
+def test_prefill_int8_refusals():
+    from paged_kv_cache_409_b200 import build
+    build.build()
+    fn = pkv.load_library().pkv_paged_attention_prefill_chunk_int8
+    P = 1 << 20
+
+    def pre(**kw):
+        a = dict(out=P, q=P, kc=P, vc=P, bt=P, sl=P, qsl=P, R=0, Tq=4, mq=4, scale=0.1, Hq=4, Hkv=2, D=64, B=16, MB=4, NB=8,
+                 dt=1)
+        a.update(kw)
+        return fn(*a.values(), None)
+
+    assert pre() == 0 and pre(R=1, Tq=0) == 0 and pre(R=1, mq=0) == 0
+    for kw in (dict(dt=0), dict(dt=3), dict(dt=4), dict(D=96), dict(B=64), dict(Hq=6), dict(Hq=32)):
+        assert pre(**kw) == EUNSUPPORTED, kw
+    for kw in (dict(R=-1), dict(Tq=-1), dict(mq=-1), dict(Hq=5), dict(NB=0), dict(MB=0), dict(scale=float("inf")),
+               dict(R=1, q=0), dict(R=1, vc=P + 8), dict(R=1, qsl=P + 2)):
+        assert pre(**kw) == EINVAL, kw
