@@ -53,16 +53,19 @@ typedef enum { PKV_F32 = 0, PKV_F16 = 1, PKV_BF16 = 2, PKV_FP8_E4M3 = 3 } pkv_dt
 
 /* Pools of 8-bit rows ("int8 pools"), a further pool type, used by the calls
  * named *_int8 (and as the dtype of pkv_decode_partition_size).  A row is one
- * token's head_dim elements of one KV head, stored as one-byte codes
- *     u = 128 + rint(x / s)    (fp32 quotient, ties to even)
- * with a scale of its own, s = max |x| / 127 in fp32, and stands for
- * s * (u - 128).  No calibration is needed: every row uses its full range.
+ * token's head_dim elements of one KV head, stored as one-byte codes with a
+ * scale of its own, s = max |x| * (1 / 127) in fp32:
+ *     u = 128 + round(127 x / max |x|)
+ * (to nearest; a quotient within 2^-21 of itself of a tie may go either way),
+ * and stands for s * (u - 128).  No calibration is needed: every row uses its
+ * full range.
  * The bytes of a block are the codes [block_size, num_kv_heads, head_dim] and
  * then the scales, float [num_kv_heads, block_size]:
  * pkv_int8_block_bytes(...) = block_size * num_kv_heads * (head_dim + 4) in
  * all, so pkv_copy_blocks and pkv_swap_blocks move whole blocks with that
- * block_bytes.  s is at least 2^-80 (a zero row has codes 128); a row that
- * holds a NaN or an infinity gets the scale NaN and reads as NaN. */
+ * block_bytes.  s is at least 2^-80 (smaller rows are coded with that step, a
+ * zero row's codes are 128); a row that holds a NaN or an infinity gets the
+ * scale NaN (its codes are then unspecified) and reads as NaN. */
 #define PKV_INT8 4
 
 typedef enum {

@@ -153,8 +153,8 @@ def load_library():
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the current stream's handle, without building a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -168,11 +168,23 @@ def _dev(t: torch.Tensor, name: str) -> int:
     return t.data_ptr()
 
 
-def _here(t: torch.Tensor, name: str) -> int:
-    """As :func:`_dev`, for a tensor that must live on the current device."""
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
+def _device(t: torch.Tensor, name: str) -> int:
+    """Device index of a call's first tensor, which must be the current device."""
+    dev = t.get_device()
+    if dev < 0:
+        _dev(t, name)  # not a CUDA tensor
+    elif dev != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return _dev(t, name)
+    return dev
+
+
+def _at(t: torch.Tensor, name: str, dev: int) -> int:
+    """Pointer of a contiguous tensor on device ``dev``."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the call's other tensors, not on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _code(t: torch.Tensor) -> int:
@@ -535,60 +547,67 @@ def rope_table(cos_sin, base=10000.0, first_position=0, scaling="none", factor=1
     """Fill ``cos_sin`` (fp32 ``[positions, rotary_dim]``) with the rotary table's rows from ``first_position`` on:
     the cosines, then the sines, of ``position * theta_i``, times ``attention_factor``.  ``scaling``: "none",
     "linear", "ntk" or "by_parts" (see ``pkv_rope_table``)."""
-    lib = load_library()
+    lib = _lib or load_library()
     if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
         raise ValueError("cos_sin must be a float32 [positions, rotary_dim] tensor")
     if scaling not in ROPE_SCALING:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}")
-    spec = RopeSpec(float(base), float(factor), float(alpha), float(beta), float(attention_factor),
-                    int(original_max_position), cos_sin.shape[1], ROPE_SCALING[scaling])
-    rc = lib.pkv_rope_table(_here(cos_sin, "cos_sin"), int(first_position), cos_sin.shape[0], ctypes.byref(spec),
+    n, rotary_dim = cos_sin.shape
+    spec = RopeSpec(base, factor, alpha, beta, attention_factor, original_max_position, rotary_dim, ROPE_SCALING[scaling])
+    rc = lib.pkv_rope_table(_at(cos_sin, "cos_sin", _device(cos_sin, "cos_sin")), first_position, n, ctypes.byref(spec),
                             _stream(stream))
     _ok(rc, "rope_table")
     return cos_sin
 
 
-def _head_rows(t: torch.Tensor, name: str):
+def _head_rows(t: torch.Tensor, name: str, dev: int, T: int, H: int, D: int):
     """(pointer, elements between tokens) of ``[T, H, D]`` rows whose heads are contiguous within a token, as in a
     slice of a projection's output."""
-    T, H, D = t.shape
-    if t.stride(2) != 1 and D > 1 or t.stride(1) != D and H > 1:
+    if t.shape != (T, H, D):
+        raise ValueError(f"{name} must be [{T}, {H}, {D}]: [tokens, heads, head_dim] of the query's tokens and the pools")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the call's other tensors, not on {t.device}")
+    token, head, element = t.stride()
+    if element != 1 and D > 1 or head != D and H > 1:
         raise ValueError(f"{name}'s heads must be contiguous within a token")
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return _dev(t[:1].reshape(-1), name) if T else t.data_ptr(), t.stride(0) if T > 1 else H * D
+    return t.data_ptr(), token if T > 1 else H * D
 
 
-def _rope_and_cache(name, query_out, query, key, value, cos_sin, positions, pools, pool_shape, slot_mapping, interleaved,
-                    q_norm_weight, k_norm_weight, eps, scales, stream):
-    lib = load_library()
+def _rope_and_cache(name, query_out, query, key, value, cos_sin, positions, dev, pools, pool_shape, slot_mapping,
+                    interleaved, q_norm_weight, k_norm_weight, eps, scales, stream):
     T, Hq, D = query.shape
     NB, B, Hkv, Dp = pool_shape
-    if key.shape != (T, Hkv, D) or value.shape != (T, Hkv, D) or Dp != D:
-        raise ValueError("key and value must be [tokens, num_kv_heads, head_dim] of the query's tokens and the pools")
-    if query_out.shape != query.shape or not query_out.dtype == query.dtype == key.dtype == value.dtype:
-        raise ValueError("query_out, query, key and value must agree in dtype, query_out and query in shape")
+    dtype = query.dtype
+    if Dp != D or query_out.shape != query.shape:
+        raise ValueError("query and query_out must be [tokens, num_q_heads, head_dim] of the pools")
+    if query_out.dtype != dtype or key.dtype != dtype or value.dtype != dtype:
+        raise ValueError("query_out, query, key and value must have one dtype")
     if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
         raise ValueError("slot_mapping must be int64 [tokens]")
     rotary_dim = max_position = 0
+    table = pos = qw = kw = None
     if cos_sin is not None:
         if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
             raise ValueError("cos_sin must be a float32 [positions, rotary_dim] tensor")
         if positions is None or positions.dtype != torch.int64 or positions.shape != (T,):
             raise ValueError("positions must be int64 [tokens]")
         max_position, rotary_dim = cos_sin.shape
-    for w, what in ((q_norm_weight, "q_norm_weight"), (k_norm_weight, "k_norm_weight")):
-        if w is not None and (w.dtype != query.dtype or w.shape != (D,)):
-            raise ValueError(f"{what} must be [head_dim] in the query's dtype")
-    q, qs = _head_rows(query, "query")
-    k, ks = _head_rows(key, "key")
-    v, vs = _head_rows(value, "value")
-    opt = lambda t, what: None if t is None else _here(t, what)  # noqa: E731
-    rc = getattr(lib, "pkv_" + name)(
-        _here(query_out, "query_out"), q, k, v, qs, ks, vs, opt(q_norm_weight, "q_norm_weight"),
-        opt(k_norm_weight, "k_norm_weight"), float(eps), opt(cos_sin, "cos_sin"), max_position, rotary_dim,
-        int(bool(interleaved)), opt(positions if rotary_dim else None, "positions"), pools[0], pools[1],
-        _here(slot_mapping, "slot_mapping"), T, Hq, Hkv, D, B, NB, _code(query), *scales, _stream(stream))
+        table, pos = _at(cos_sin, "cos_sin", dev), _at(positions, "positions", dev)
+    if q_norm_weight is not None:
+        if q_norm_weight.dtype != dtype or q_norm_weight.shape != (D,):
+            raise ValueError("q_norm_weight must be [head_dim] in the query's dtype")
+        qw = _at(q_norm_weight, "q_norm_weight", dev)
+    if k_norm_weight is not None:
+        if k_norm_weight.dtype != dtype or k_norm_weight.shape != (D,):
+            raise ValueError("k_norm_weight must be [head_dim] in the query's dtype")
+        kw = _at(k_norm_weight, "k_norm_weight", dev)
+    q, qs = _head_rows(query, "query", dev, T, Hq, D)
+    k, ks = _head_rows(key, "key", dev, T, Hkv, D)
+    v, vs = _head_rows(value, "value", dev, T, Hkv, D)
+    rc = getattr(_lib or load_library(), "pkv_" + name)(
+        _at(query_out, "query_out", dev), q, k, v, qs, ks, vs, qw, kw, eps, table, max_position, rotary_dim,
+        1 if interleaved else 0, pos, pools[0], pools[1], _at(slot_mapping, "slot_mapping", dev), T, Hq, Hkv, D, B, NB,
+        _code(query), *scales, _stream(stream))
     _ok(rc, name)
     return query_out
 
@@ -600,8 +619,9 @@ def rope_and_cache(query_out, query, key, value, cos_sin, positions, key_cache, 
     ``[T, Hkv, D]`` to the pools' slots.  Query, key and value may be slices of one projection's output."""
     if key_cache.dtype != query.dtype or value_cache.dtype != query.dtype or key_cache.shape != value_cache.shape:
         raise ValueError("the pools must have the query's dtype and one shape")
-    return _rope_and_cache("rope_and_cache", query_out, query, key, value, cos_sin, positions,
-                           (_here(key_cache, "key_cache"), _here(value_cache, "value_cache")), key_cache.shape,
+    dev = _device(query, "query")
+    return _rope_and_cache("rope_and_cache", query_out, query, key, value, cos_sin, positions, dev,
+                           (_at(key_cache, "key_cache", dev), _at(value_cache, "value_cache", dev)), key_cache.shape,
                            slot_mapping, interleaved, q_norm_weight, k_norm_weight, eps, (), stream)
 
 
@@ -611,6 +631,7 @@ def rope_and_cache_fp8(query_out, query, key, value, cos_sin, positions, key_cac
     if key_cache.shape != value_cache.shape:
         raise ValueError("the pools must have one shape")
     return _rope_and_cache("rope_and_cache_fp8", query_out, query, key, value, cos_sin, positions,
+                           _device(query, "query"),
                            (_fp8_pool(key_cache, "key_cache"), _fp8_pool(value_cache, "value_cache")), key_cache.shape,
                            slot_mapping, interleaved, q_norm_weight, k_norm_weight, eps,
                            (float(k_scale), float(v_scale)), stream)
@@ -619,8 +640,8 @@ def rope_and_cache_fp8(query_out, query, key, value, cos_sin, positions, key_cac
 def rope_and_cache_int8(query_out, query, key, value, cos_sin, positions, key_cache, value_cache, slot_mapping,
                         interleaved=False, q_norm_weight=None, k_norm_weight=None, eps=1e-6, stream=None):
     """:func:`rope_and_cache` into int8 pools."""
-    shape, k, v = _int8_pools(key_cache, value_cache)
-    return _rope_and_cache("rope_and_cache_int8", query_out, query, key, value, cos_sin, positions, (k, v), shape,
+    shape, dev, k, v = _int8_pools(key_cache, value_cache)
+    return _rope_and_cache("rope_and_cache_int8", query_out, query, key, value, cos_sin, positions, dev, (k, v), shape,
                            slot_mapping, interleaved, q_norm_weight, k_norm_weight, eps, (), stream)
 
 
@@ -642,65 +663,66 @@ def int8_pool_views(pool):
 
 
 def _int8_pools(key_cache, value_cache):
-    """((NB, B, Hkv, D), key pointer, value pointer) of two int8 pools."""
-    for t, name in ((key_cache, "key_cache"), (value_cache, "value_cache")):
-        if t.dtype != torch.uint8 or t.dim() != 4 or t.shape[3] <= 4:
-            raise ValueError(f"{name} must be a uint8 [blocks, block_size, num_kv_heads, head_dim + 4] pool")
-    if key_cache.shape != value_cache.shape:
-        raise ValueError("key_cache and value_cache differ in shape")
-    NB, B, H, W = key_cache.shape
-    return (NB, B, H, W - 4), _here(key_cache, "key_cache"), _here(value_cache, "value_cache")
+    """((NB, B, Hkv, D), device, key pointer, value pointer) of two int8 pools."""
+    shape = key_cache.shape
+    if len(shape) != 4 or shape[3] <= 4 or key_cache.dtype != torch.uint8 or value_cache.dtype != torch.uint8 \
+            or value_cache.shape != shape:
+        raise ValueError("key_cache and value_cache must be uint8 [blocks, block_size, num_kv_heads, head_dim + 4] "
+                         "pools of one shape")
+    dev = _device(key_cache, "key_cache")
+    NB, B, H, W = shape
+    return (NB, B, H, W - 4), dev, _at(key_cache, "key_cache", dev), _at(value_cache, "value_cache", dev)
 
 
 def reshape_and_cache_int8(key, value, key_cache, value_cache, slot_mapping, stream=None):
     """Quantise ``key``/``value`` ``[T, Hkv, D]`` (fp32/fp16/bf16) row by row into the int8 pools' slots
     ``slot_mapping`` (int64, -1 = skip)."""
-    lib = load_library()
-    (NB, B, H, D), k, v = _int8_pools(key_cache, value_cache)
+    (NB, B, H, D), dev, k, v = _int8_pools(key_cache, value_cache)
     T = slot_mapping.numel()
     if slot_mapping.dtype != torch.int64:
         raise ValueError("slot_mapping must be int64")
     if key.shape != (T, H, D) or value.shape != (T, H, D) or key.dtype != value.dtype:
         raise ValueError("key and value must be [tokens, num_kv_heads, head_dim] of the pools, in one dtype")
-    rc = lib.pkv_reshape_and_cache_int8(_here(key, "key"), _here(value, "value"), k, v,
-                                        _here(slot_mapping, "slot_mapping"), T, H, D, B, NB, _code(key),
-                                        _stream(stream))
+    rc = (_lib or load_library()).pkv_reshape_and_cache_int8(
+        _at(key, "key", dev), _at(value, "value", dev), k, v, _at(slot_mapping, "slot_mapping", dev), T, H, D, B, NB,
+        _code(key), _stream(stream))
     _ok(rc, "reshape_and_cache_int8")
 
 
 def read_cache_int8(key_out, value_out, key_cache, value_cache, slot_mapping, stream=None):
     """The rows of ``slot_mapping``'s slots of two int8 pools as values, into ``key_out``/``value_out``
     ``[T, Hkv, D]`` (fp32/fp16/bf16); the rows of negative slots are left as they were."""
-    lib = load_library()
-    (NB, B, H, D), k, v = _int8_pools(key_cache, value_cache)
+    (NB, B, H, D), dev, k, v = _int8_pools(key_cache, value_cache)
     T = slot_mapping.numel()
     if slot_mapping.dtype != torch.int64:
         raise ValueError("slot_mapping must be int64")
     if key_out.shape != (T, H, D) or value_out.shape != (T, H, D) or key_out.dtype != value_out.dtype:
         raise ValueError("key_out and value_out must be [tokens, num_kv_heads, head_dim] of the pools, in one dtype")
-    rc = lib.pkv_read_cache_int8(_here(key_out, "key_out"), _here(value_out, "value_out"), k, v,
-                                 _here(slot_mapping, "slot_mapping"), T, H, D, B, NB, _code(key_out), _stream(stream))
+    rc = (_lib or load_library()).pkv_read_cache_int8(
+        _at(key_out, "key_out", dev), _at(value_out, "value_out", dev), k, v, _at(slot_mapping, "slot_mapping", dev), T, H,
+        D, B, NB, _code(key_out), _stream(stream))
     _ok(rc, "read_cache_int8")
     return key_out, value_out
 
 
 def _int8_decode_args(out, query, key_cache, value_cache, block_tables, context_lens, max_context_len, partition_size,
                       workspace, total_context_tokens):
-    """The arguments shared by the int8 decode and its step: (out, query, pools, tables) pointers, the sizes, the
-    partition and the workspace."""
-    (NB, B, Hkv, D), k, v = _int8_pools(key_cache, value_cache)
+    """The arguments shared by the int8 decode and its step: the device, (out, query, pools, tables) pointers, the
+    sizes, the partition and the workspace."""
+    (NB, B, Hkv, D), dev, k, v = _int8_pools(key_cache, value_cache)
     S, Hq, Dq = query.shape
     if Dq != D or out.shape != query.shape or out.dtype != query.dtype:
         raise ValueError("out and query must be [num_seqs, num_q_heads, head_dim] of the pools, in one dtype")
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise ValueError("block_tables and context_lens must be int32")
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != S or context_lens.shape != (S,):
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq] and context_lens [num_seqs]")
     part, ws_ptr, ws_bytes = _decode_workspace(S, Hq, Hkv, D, B, max_context_len, INT8, partition_size, workspace,
                                                query.device, total_context_tokens)
-    return ((_here(out, "out"), _here(query, "query"), k, v, _here(block_tables, "block_tables"),
-             _here(context_lens, "context_lens")),
-            (S, Hq, Hkv, D, B, block_tables.shape[1], NB, int(max_context_len), part, _code(query), ws_ptr, ws_bytes))
+    return (dev, (_at(out, "out", dev), _at(query, "query", dev), k, v, _at(block_tables, "block_tables", dev),
+                  _at(context_lens, "context_lens", dev)),
+            (S, Hq, Hkv, D, B, tables[1], NB, int(max_context_len), part, _code(query), ws_ptr, ws_bytes))
 
 
 def paged_attention_decode_int8(out, query, key_cache, value_cache, block_tables, context_lens, scale,
@@ -708,11 +730,10 @@ def paged_attention_decode_int8(out, query, key_cache, value_cache, block_tables
                                 total_context_tokens=0):
     """Decode attention over int8 pools (uint8 ``[NB, B, Hkv, D + 4]``); ``out``/``query`` ``[S, Hq, D]`` in fp16 or
     bf16, the other arguments as for :func:`paged_attention_decode`."""
-    lib = load_library()
-    ptrs, sizes = _int8_decode_args(out, query, key_cache, value_cache, block_tables, context_lens, max_context_len,
-                                    partition_size, workspace, total_context_tokens)
-    _ok(lib.pkv_paged_attention_decode_int8(*ptrs, float(scale), *sizes, _stream(stream)),
-        "paged_attention_decode_int8")
+    load_library()
+    _, ptrs, sizes = _int8_decode_args(out, query, key_cache, value_cache, block_tables, context_lens, max_context_len,
+                                       partition_size, workspace, total_context_tokens)
+    _ok(_lib.pkv_paged_attention_decode_int8(*ptrs, scale, *sizes, _stream(stream)), "paged_attention_decode_int8")
     return out
 
 
@@ -720,17 +741,18 @@ def paged_attention_decode_step_int8(new_keys, new_values, slot_mapping, out, qu
                                      block_tables, context_lens, scale, max_context_len, partition_size=None,
                                      workspace=None, stream=None, total_context_tokens=0):
     """The decode step over int8 pools: ``reshape_and_cache_int8`` then ``paged_attention_decode_int8``."""
-    lib = load_library()
-    ptrs, sizes = _int8_decode_args(out, query, key_cache, value_cache, block_tables, context_lens, max_context_len,
-                                    partition_size, workspace, total_context_tokens)
-    T, rows = slot_mapping.numel(), (slot_mapping.numel(), *sizes[2:4])
+    load_library()
+    dev, ptrs, sizes = _int8_decode_args(out, query, key_cache, value_cache, block_tables, context_lens,
+                                         max_context_len, partition_size, workspace, total_context_tokens)
+    T = slot_mapping.numel()
+    rows = (T, sizes[2], sizes[3])
     if slot_mapping.dtype != torch.int64:
         raise ValueError("slot_mapping must be int64")
     if new_keys.shape != rows or new_values.shape != rows or not new_keys.dtype == new_values.dtype == query.dtype:
         raise ValueError("new_keys and new_values must be [tokens, num_kv_heads, head_dim] in the query's dtype")
-    rc = lib.pkv_paged_attention_decode_step_int8(_here(new_keys, "new_keys"), _here(new_values, "new_values"),
-                                                  _here(slot_mapping, "slot_mapping"), T, *ptrs, float(scale), *sizes,
-                                                  _stream(stream))
+    rc = _lib.pkv_paged_attention_decode_step_int8(_at(new_keys, "new_keys", dev), _at(new_values, "new_values", dev),
+                                                   _at(slot_mapping, "slot_mapping", dev), T, *ptrs, scale, *sizes,
+                                                   _stream(stream))
     _ok(rc, "paged_attention_decode_step_int8")
     return out
 
@@ -739,21 +761,20 @@ def paged_attention_prefill_chunk_int8(out, query, key_cache, value_cache, block
                                        max_q_len, scale, stream=None):
     """Causal chunked prefill over int8 pools (uint8 ``[NB, B, Hkv, D + 4]``); ``out``/``query`` packed
     ``[sum n_r, Hq, D]`` in fp16 or bf16."""
-    lib = load_library()
-    (NB, B, Hkv, D), k, v = _int8_pools(key_cache, value_cache)
+    (NB, B, Hkv, D), dev, k, v = _int8_pools(key_cache, value_cache)
     Tq, Hq, Dq = query.shape
     R = seq_lens.numel()
     if Dq != D or out.shape != query.shape or out.dtype != query.dtype:
         raise ValueError("out and query must be [tokens, num_q_heads, head_dim] of the pools, in one dtype")
-    for t, name in ((block_tables, "block_tables"), (seq_lens, "seq_lens"), (query_start_loc, "query_start_loc")):
-        if t.dtype != torch.int32:
-            raise ValueError(f"{name} must be int32")
-    if block_tables.dim() != 2 or block_tables.shape[0] != R or query_start_loc.numel() != R + 1:
+    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32 or query_start_loc.dtype != torch.int32:
+        raise ValueError("block_tables, seq_lens and query_start_loc must be int32")
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != R or query_start_loc.numel() != R + 1:
         raise ValueError("block_tables must be [chunks, max_blocks_per_seq] and query_start_loc [chunks + 1]")
-    rc = lib.pkv_paged_attention_prefill_chunk_int8(
-        _here(out, "out"), _here(query, "query"), k, v, _here(block_tables, "block_tables"),
-        _here(seq_lens, "seq_lens"), _here(query_start_loc, "query_start_loc"), R, Tq, int(max_q_len), float(scale),
-        Hq, Hkv, D, B, block_tables.shape[1], NB, _code(query), _stream(stream))
+    rc = (_lib or load_library()).pkv_paged_attention_prefill_chunk_int8(
+        _at(out, "out", dev), _at(query, "query", dev), k, v, _at(block_tables, "block_tables", dev),
+        _at(seq_lens, "seq_lens", dev), _at(query_start_loc, "query_start_loc", dev), R, Tq, max_q_len, scale, Hq, Hkv, D, B,
+        tables[1], NB, _code(query), _stream(stream))
     _ok(rc, "paged_attention_prefill_chunk_int8")
     return out
 

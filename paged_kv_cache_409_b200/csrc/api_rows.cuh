@@ -7,6 +7,9 @@ namespace {
 // Lanes per row of head_dim elements, eight elements each.
 int row_lanes(int head_dim) { return head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32; }
 
+// A row call's grid counts tokens in x and blocks of heads in y.
+constexpr int kMaxRowHeads = 1 << 15;
+
 // The shape rules of int8 pools: 16-byte rows of codes and 16-byte blocks.
 bool int8_shape(int num_kv_heads, int head_dim, int block_size) {
     return head_dim % 16 == 0 && head_dim <= 256 && (int64_t)block_size * num_kv_heads % 4 == 0 &&
@@ -32,6 +35,7 @@ int rows_int8_check(const void* x, const void* y, const void* key_cache, const v
     if (num_tokens < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0) return PKV_EINVAL;
     if (!int8_shape(num_kv_heads, head_dim, block_size)) return PKV_EUNSUPPORTED;
     if (num_tokens == 0) return PKV_OK;
+    if (num_tokens > INT32_MAX || num_kv_heads > kMaxRowHeads) return PKV_EUNSUPPORTED;
     if (!x || !y || !key_cache || !value_cache || !slot_mapping) return PKV_EINVAL;
     if (!aligned16(x) || !aligned16(y) || !aligned16(key_cache) || !aligned16(value_cache) ||
         (reinterpret_cast<uintptr_t>(slot_mapping) & 7))
@@ -39,42 +43,93 @@ int rows_int8_check(const void* x, const void* y, const void* key_cache, const v
     return PKV_OK;
 }
 
-template <typename TS>
-int launch_append_int8(const void* key, const void* value, void* kc, void* vc, const int64_t* slots, int64_t tokens,
-                       int heads, int dim, int block_size, int64_t num_slots, cudaStream_t s) {
-    const int lanes = row_lanes(dim);
-    const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(tokens * 2 * heads, 128 / lanes), 1 << 20);
-    auto kern = lanes == 8    ? pkv::append_int8_kernel<TS, 8>
-                : lanes == 16 ? pkv::append_int8_kernel<TS, 16>
-                              : pkv::append_int8_kernel<TS, 32>;
-    kern<<<grid, 128, 0, s>>>(static_cast<const TS*>(key), static_cast<const TS*>(value), static_cast<uint8_t*>(kc),
-                              static_cast<uint8_t*>(vc), slots, tokens, heads, dim, block_size, num_slots);
+int log2_ceil(int64_t n) {
+    int k = 0;
+    while ((int64_t(1) << k) < n) ++k;
+    return k;
+}
+
+#ifndef PKV_ROW_UNROLL
+#define PKV_ROW_UNROLL 4  // rows per thread of a large append or read
+#endif
+// Rows per thread: PKV_ROW_UNROLL keep more bytes in flight once there are
+// enough rows for it, two spread a small batch over the SMs.
+bool many_rows(int64_t tokens, int heads, int per) {
+    return tokens * heads >= (int64_t)per * PKV_ROW_UNROLL * 4 * sm_count();
+}
+
+#ifndef PKV_ROPE_UNROLL
+#define PKV_ROPE_UNROLL 2  // rows per thread of norm + rotation + append
+#endif
+
+template <typename T, int kPool, int E, int LPR, int U, bool kPlain, bool kNorm, bool kInterleaved>
+int launch_rows(pkv::RopeRowsParams p, cudaStream_t s) {
+    constexpr int kPer = 128 / LPR;
+    const int most = log2_ceil(kPer);
+    p.q_shift = std::min(most, log2_ceil(std::max(p.num_q_heads, 1)));
+    p.kv_shift = std::min(most, log2_ceil(p.num_kv_heads));
+    p.q_blocks = kPlain ? 0 : (int)ceil_div(p.num_q_heads, (int64_t)U << p.q_shift);
+    const int64_t kv_blocks = ceil_div(p.num_kv_heads, (int64_t)(U / 2) << p.kv_shift);
+    const int64_t groups = ceil_div(p.num_tokens, kPer >> (kPlain ? p.kv_shift : std::max(p.q_shift, p.kv_shift)));
+    const dim3 grid((unsigned)groups, (unsigned)(p.q_blocks + kv_blocks));
+    pkv::rope_rows_kernel<T, kPool, E, LPR, U, kPlain, kNorm, kInterleaved><<<grid, 128, 0, s>>>(p);
+    PKV_CUDA(cudaGetLastError());
+    return PKV_OK;
+}
+
+template <typename T, int kPool, bool kNorm, bool kInterleaved>
+int launch_rope_as(const pkv::RopeRowsParams& p, cudaStream_t s) {
+    constexpr int U = PKV_ROPE_UNROLL;
+    // eight-element vectors need rows, and the rotated halves of the half
+    // layout, in multiples of sixteen; the rest goes by four (one variant)
+    if (p.head_dim % 16 || p.rotary_dim % 16)
+        return launch_rows<T, kPool, 4, 32, U, false, kNorm, kInterleaved>(p, s);
+    if (p.head_dim <= 64) return launch_rows<T, kPool, 8, 4, U, false, kNorm, kInterleaved>(p, s);
+    if (p.head_dim <= 128) return launch_rows<T, kPool, 8, 8, U, false, kNorm, kInterleaved>(p, s);
+    return launch_rows<T, kPool, 8, 16, U, false, kNorm, kInterleaved>(p, s);
+}
+
+template <typename T, int U>
+int launch_append_as(const pkv::RopeRowsParams& p, cudaStream_t s) {
+    constexpr int kPool = pkv::kPoolInt8;
+    if (p.head_dim <= 64) return launch_rows<T, kPool, 8, 4, U, true, false, false>(p, s);
+    if (p.head_dim <= 128) return launch_rows<T, kPool, 8, 8, U, true, false, false>(p, s);
+    return launch_rows<T, kPool, 8, 16, U, true, false, false>(p, s);
+}
+
+template <typename T>
+int launch_append_int8(const pkv::RopeRowsParams& p, cudaStream_t s) {
+    return many_rows(p.num_tokens, 2 * p.num_kv_heads, 256 / row_lanes(p.head_dim))
+               ? launch_append_as<T, PKV_ROW_UNROLL>(p, s)
+               : launch_append_as<T, 2>(p, s);
+}
+
+template <typename T, int kPool>
+int launch_rope(const pkv::RopeRowsParams& p, bool interleaved, cudaStream_t s) {
+    if (p.q_weight || p.k_weight)
+        return interleaved ? launch_rope_as<T, kPool, true, true>(p, s) : launch_rope_as<T, kPool, true, false>(p, s);
+    return interleaved ? launch_rope_as<T, kPool, false, true>(p, s) : launch_rope_as<T, kPool, false, false>(p, s);
+}
+
+template <typename TD, int LPR, int U>
+int launch_read_u(pkv::ReadRowsParams p, cudaStream_t s) {
+    constexpr int kPer = 128 / LPR;
+    p.shift = std::min(log2_ceil(kPer), log2_ceil(p.num_kv_heads));
+    const dim3 grid((unsigned)ceil_div(p.num_tokens, kPer >> p.shift),
+                    (unsigned)ceil_div(p.num_kv_heads, (int64_t)(U / 2) << p.shift));
+    pkv::read_int8_kernel<TD, LPR, U><<<grid, 128, 0, s>>>(p);
     PKV_CUDA(cudaGetLastError());
     return PKV_OK;
 }
 
 template <typename TD>
-int launch_read_int8(void* key, void* value, const void* kc, const void* vc, const int64_t* slots, int64_t tokens,
-                     int heads, int dim, int block_size, int64_t num_slots, cudaStream_t s) {
-    const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(tokens * 2 * heads * (dim / 8), 128), 1 << 20);
-    pkv::read_int8_kernel<TD><<<grid, 128, 0, s>>>(static_cast<TD*>(key), static_cast<TD*>(value),
-                                                   static_cast<const uint8_t*>(kc), static_cast<const uint8_t*>(vc),
-                                                   slots, tokens, heads, dim, block_size, num_slots);
-    PKV_CUDA(cudaGetLastError());
-    return PKV_OK;
-}
-
-template <typename T, int kPool>
-int launch_rope(const pkv::RopeRowsParams& p, cudaStream_t s) {
-    const int lanes = row_lanes(p.head_dim);
-    const int rows = p.num_q_heads + 2 * p.num_kv_heads;
-    const dim3 grid((unsigned)p.num_tokens, (unsigned)std::min<int64_t>(ceil_div(rows, 128 / lanes), 65535));
-    auto kern = lanes == 8    ? pkv::rope_rows_kernel<T, kPool, 8>
-                : lanes == 16 ? pkv::rope_rows_kernel<T, kPool, 16>
-                              : pkv::rope_rows_kernel<T, kPool, 32>;
-    kern<<<grid, 128, 0, s>>>(p);
-    PKV_CUDA(cudaGetLastError());
-    return PKV_OK;
+int launch_read(const pkv::ReadRowsParams& p, cudaStream_t s) {
+    constexpr int U = PKV_ROW_UNROLL;
+    const int lanes = row_lanes(p.head_dim) / 2;
+    const bool many = many_rows(p.num_tokens, 2 * p.num_kv_heads, 128 / lanes);
+    if (lanes == 4) return many ? launch_read_u<TD, 4, U>(p, s) : launch_read_u<TD, 4, 2>(p, s);
+    if (lanes == 8) return many ? launch_read_u<TD, 8, U>(p, s) : launch_read_u<TD, 8, 2>(p, s);
+    return many ? launch_read_u<TD, 16, U>(p, s) : launch_read_u<TD, 16, 2>(p, s);
 }
 
 template <typename T, int D, int G>
@@ -130,8 +185,7 @@ int rope_impl(void* query_out, const void* query, const void* key, const void* v
     if (kPool == pkv::kPoolE4M3 && head_dim % 16) return PKV_EUNSUPPORTED;
     if (kPool == pkv::kPoolInt8 && !int8_shape(num_kv_heads, head_dim, block_size)) return PKV_EUNSUPPORTED;
     if (num_tokens == 0) return PKV_OK;
-    if (num_tokens > INT32_MAX || (int64_t)num_q_heads + 2 * (int64_t)num_kv_heads > INT32_MAX / 256)
-        return PKV_EUNSUPPORTED;
+    if (num_tokens > INT32_MAX || num_q_heads > kMaxRowHeads || num_kv_heads > kMaxRowHeads) return PKV_EUNSUPPORTED;
     if (!query_out || !query || !key || !value || !key_cache || !value_cache || !slot_mapping) return PKV_EINVAL;
     if (rotary_dim > 0 && (!cos_sin || !positions)) return PKV_EINVAL;
     const int eb = elem_bytes(dtype);
@@ -163,10 +217,10 @@ int rope_impl(void* query_out, const void* query, const void* key, const void* v
     p.q_stride = query_stride, p.k_stride = key_stride, p.v_stride = value_stride;
     p.q_weight = q_norm_weight, p.k_weight = k_norm_weight;
     p.eps = eps;
+    p.inv_dim = 1.f / head_dim;
     p.cos_sin = cos_sin;
     p.max_position = max_position;
     p.rotary_dim = rotary_dim;
-    p.interleaved = interleaved != 0;
     p.positions = rotary_dim > 0 ? positions : nullptr;
     p.key_cache = key_cache, p.value_cache = value_cache;
     p.slot_mapping = slot_mapping;
@@ -174,9 +228,9 @@ int rope_impl(void* query_out, const void* query, const void* key, const void* v
     p.num_q_heads = num_q_heads, p.num_kv_heads = num_kv_heads, p.head_dim = head_dim, p.block_size = block_size;
     p.k_scale = k_scale, p.v_scale = v_scale;
     switch (dtype) {
-        case PKV_F32: return launch_rope<float, kPool>(p, s);
-        case PKV_F16: return launch_rope<__half, kPool>(p, s);
-        default: return launch_rope<__nv_bfloat16, kPool>(p, s);
+        case PKV_F32: return launch_rope<float, kPool>(p, interleaved != 0, s);
+        case PKV_F16: return launch_rope<__half, kPool>(p, interleaved != 0, s);
+        default: return launch_rope<__nv_bfloat16, kPool>(p, interleaved != 0, s);
     }
 }
 
@@ -221,8 +275,9 @@ int pkv_rope_table(float* cos_sin, int64_t first_position, int64_t num_positions
         }
         p.turns[i] = theta / pi;
     }
-    const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(num_positions * p.half, 256), 1 << 20);
-    pkv::rope_table_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    const int64_t threads = ceil_div(num_positions, pkv::kRopeTableRows) * p.half;
+    const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(threads, 128), 1 << 20);
+    pkv::rope_table_kernel<<<grid, 128, 0, static_cast<cudaStream_t>(stream)>>>(p);
     PKV_CUDA(cudaGetLastError());
     return PKV_OK;
 }
@@ -280,11 +335,18 @@ int pkv_reshape_and_cache_int8(const void* key, const void* value, void* key_cac
     const int64_t num_slots = num_blocks * block_size;
     rc = check_slots(slot_mapping, num_tokens, num_slots, s);
     if (rc) return rc;
-    auto launch = src_dtype == PKV_F32   ? launch_append_int8<float>
-                  : src_dtype == PKV_F16 ? launch_append_int8<__half>
-                                         : launch_append_int8<__nv_bfloat16>;
-    return launch(key, value, key_cache, value_cache, slot_mapping, num_tokens, num_kv_heads, head_dim, block_size,
-                  num_slots, s);
+    pkv::RopeRowsParams p = {};
+    p.key = key, p.value = value;
+    p.k_stride = p.v_stride = (int64_t)num_kv_heads * head_dim;
+    p.key_cache = key_cache, p.value_cache = value_cache;
+    p.slot_mapping = slot_mapping;
+    p.num_tokens = num_tokens, p.num_slots = num_slots;
+    p.num_kv_heads = num_kv_heads, p.head_dim = head_dim, p.block_size = block_size;
+    switch (src_dtype) {
+        case PKV_F32: return launch_append_int8<float>(p, s);
+        case PKV_F16: return launch_append_int8<__half>(p, s);
+        default: return launch_append_int8<__nv_bfloat16>(p, s);
+    }
 }
 
 int pkv_read_cache_int8(void* key_out, void* value_out, const void* key_cache, const void* value_cache,
@@ -297,11 +359,14 @@ int pkv_read_cache_int8(void* key_out, void* value_out, const void* key_cache, c
     const int64_t num_slots = num_blocks * block_size;
     rc = check_slots(slot_mapping, num_tokens, num_slots, s);
     if (rc) return rc;
-    auto launch = dst_dtype == PKV_F32   ? launch_read_int8<float>
-                  : dst_dtype == PKV_F16 ? launch_read_int8<__half>
-                                         : launch_read_int8<__nv_bfloat16>;
-    return launch(key_out, value_out, key_cache, value_cache, slot_mapping, num_tokens, num_kv_heads, head_dim,
-                  block_size, num_slots, s);
+    const pkv::ReadRowsParams p = {key_out, value_out, static_cast<const uint8_t*>(key_cache),
+                                   static_cast<const uint8_t*>(value_cache), slot_mapping, num_tokens, num_slots,
+                                   num_kv_heads, head_dim, block_size, 0};
+    switch (dst_dtype) {
+        case PKV_F32: return launch_read<float>(p, s);
+        case PKV_F16: return launch_read<__half>(p, s);
+        default: return launch_read<__nv_bfloat16>(p, s);
+    }
 }
 
 int pkv_paged_attention_decode_int8(void* out, const void* query, const void* key_cache, const void* value_cache,
