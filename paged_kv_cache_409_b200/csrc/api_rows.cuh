@@ -132,9 +132,27 @@ int launch_read(const pkv::ReadRowsParams& p, cudaStream_t s) {
     return many ? launch_read_u<TD, 16, U>(p, s) : launch_read_u<TD, 16, 2>(p, s);
 }
 
+// CTAs that share an item's key tiles (a cluster of 1, 2, 4 or 8).  Measured on
+// B200: a key tile takes a CTA about 2.4 us, its start and end 9 us alone and
+// 13 us with the cluster's merge, and an SM holds one CTA.  So a launch of few
+// items is cut (8 items of 16385 keys, head_dim 128: 293 us in one part, 51 in
+// eight), one that fills the SMs is not (256 items of up to 66 tiles: 175 us in
+// one part, 202 in two).  The lengths are not known here: max_tiles is the
+// table's reach.
+int prefill_parts(int64_t items, int64_t max_tiles) {
+    int best = 1;
+    double best_us = 0;
+    for (int parts = 1; parts <= 8; parts *= 2) {
+        const double waves = std::max(1.0, (double)(items * parts) / sm_count());
+        const double us = waves * ((parts == 1 ? 9.0 : 13.0) + 2.4 * ceil_div(max_tiles, parts));
+        if (parts == 1 || us < 0.9 * best_us) best = parts, best_us = us;
+    }
+    return best;
+}
+
 template <typename T, int D, int G>
 int launch_prefill_int8(const pkv::PrefillInt8Params& prm, const CUtensorMap& tq, const CUtensorMap& tk,
-                        const CUtensorMap& tv, int grid, cudaStream_t s) {
+                        const CUtensorMap& tv, int items, int parts, cudaStream_t s) {
     using C = pkv::PrefillInt8Cfg<D, G>;
     auto kern = pkv::paged_prefill_int8_kernel<T, D, G>;
     int dev = 0;
@@ -149,19 +167,30 @@ int launch_prefill_int8(const pkv::PrefillInt8Params& prm, const CUtensorMap& tq
         PKV_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
         configured[dev & 63] = true;
     }
-    kern<<<grid, pkv::kPrefillInt8Threads, C::SMEM, s>>>(prm, tq, tk, tv);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items * parts));
+    cfg.blockDim = dim3(pkv::kPrefillInt8Threads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = parts;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    PKV_CUDA(cudaLaunchKernelEx(&cfg, kern, prm, tq, tk, tv));
     PKV_CUDA(cudaGetLastError());
     return PKV_OK;
 }
 
 template <typename T, int D>
 int prefill_int8_by_group(int group, const pkv::PrefillInt8Params& prm, const CUtensorMap& tq, const CUtensorMap& tk,
-                          const CUtensorMap& tv, int grid, cudaStream_t s) {
+                          const CUtensorMap& tv, int items, int parts, cudaStream_t s) {
     switch (group) {
-        case 1: return launch_prefill_int8<T, D, 1>(prm, tq, tk, tv, grid, s);
-        case 2: return launch_prefill_int8<T, D, 2>(prm, tq, tk, tv, grid, s);
-        case 4: return launch_prefill_int8<T, D, 4>(prm, tq, tk, tv, grid, s);
-        case 8: return launch_prefill_int8<T, D, 8>(prm, tq, tk, tv, grid, s);
+        case 1: return launch_prefill_int8<T, D, 1>(prm, tq, tk, tv, items, parts, s);
+        case 2: return launch_prefill_int8<T, D, 2>(prm, tq, tk, tv, items, parts, s);
+        case 4: return launch_prefill_int8<T, D, 4>(prm, tq, tk, tv, items, parts, s);
+        case 8: return launch_prefill_int8<T, D, 8>(prm, tq, tk, tv, items, parts, s);
         default: return PKV_EUNSUPPORTED;
     }
 }
@@ -435,8 +464,11 @@ int pkv_paged_attention_prefill_chunk_int8(void* out, const void* query, const v
         return PKV_EINVAL;
     const int tile_tokens = 128 / group;
     const int64_t tile_pairs = ceil_div(ceil_div(max_q_len, tile_tokens), 2);
-    const int64_t grid = (int64_t)num_chunks * tile_pairs * num_kv_heads;
-    if (grid > INT32_MAX) return PKV_EUNSUPPORTED;
+    const int64_t items = (int64_t)num_chunks * tile_pairs * num_kv_heads;
+    if (items > INT32_MAX / 8) return PKV_EUNSUPPORTED;
+    // at most a last, short pair per chunk beyond the rows' worth of pairs
+    const int64_t pairs = std::min(num_chunks * tile_pairs, num_chunks + total_q_tokens / (2 * tile_tokens));
+    const int parts = prefill_parts(pairs * num_kv_heads, ceil_div((int64_t)max_blocks_per_seq * block_size, 128));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (checked_mode()) {
         std::vector<int32_t> qsl, lens;
@@ -480,10 +512,10 @@ int pkv_paged_attention_prefill_chunk_int8(void* out, const void* query, const v
     prm.block_bytes = pkv::int8_block_bytes(block_size, num_kv_heads, head_dim);
     const bool bf16 = dtype == PKV_BF16;
     if (head_dim == 64)
-        return bf16 ? prefill_int8_by_group<__nv_bfloat16, 64>(group, prm, tq, tk, tv, (int)grid, s)
-                    : prefill_int8_by_group<__half, 64>(group, prm, tq, tk, tv, (int)grid, s);
-    return bf16 ? prefill_int8_by_group<__nv_bfloat16, 128>(group, prm, tq, tk, tv, (int)grid, s)
-                : prefill_int8_by_group<__half, 128>(group, prm, tq, tk, tv, (int)grid, s);
+        return bf16 ? prefill_int8_by_group<__nv_bfloat16, 64>(group, prm, tq, tk, tv, (int)items, parts, s)
+                    : prefill_int8_by_group<__half, 64>(group, prm, tq, tk, tv, (int)items, parts, s);
+    return bf16 ? prefill_int8_by_group<__nv_bfloat16, 128>(group, prm, tq, tk, tv, (int)items, parts, s)
+                : prefill_int8_by_group<__half, 128>(group, prm, tq, tk, tv, (int)items, parts, s);
 }
 
 }  // extern "C"

@@ -41,10 +41,6 @@ struct DecodeParams {
     int64_t num_blocks;
     int partition_blocks;  // PB
     int num_partitions;    // P (grid extent)
-    // int8 pools: the scales of block 0 (after its codes) and the bytes from block to block
-    const uint8_t* k_scales;
-    const uint8_t* v_scales;
-    int64_t block_bytes;
 };
 
 template <typename T, int D, int B, int G, int NST, int NW>

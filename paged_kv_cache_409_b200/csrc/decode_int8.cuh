@@ -23,11 +23,12 @@
 //     puts 0x64 over a code (the f16 1024 + v), a subtraction of 1152 leaves
 //     v - 128, exact.
 //
-// Every row past the context, of a bad block or of an unloaded one has weight
-// 0 and codes that are finite f16 values, so V needs no masking.  A row whose
-// scale is NaN makes the result NaN.  Partitions, per-warp TMA pipelines and
-// the CTA merge are those of decode.cuh; a block's scales (one KV head's) come
-// with its codes as two bulk copies of 4 B bytes on the same barrier.
+// Every row past the context has weight 0 and codes that are finite f16
+// values, so V needs no masking; a bad block (flagged) reads as zeros.  A row
+// whose scale is NaN makes the result NaN.  Partitions, per-warp TMA pipelines
+// and the CTA merge are those of decode.cuh; a block's scales (one KV head's)
+// come through tensor maps of their own, with the codes' coordinates and on the
+// same barrier.
 #pragma once
 
 #include "decode.cuh"
@@ -56,13 +57,19 @@ __device__ __forceinline__ void mma_16832_u8s8(int (&c)[4], const uint32_t (&a)[
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes).
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
+__device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                                 uint64_t* bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
 }
+
+// The tensor maps of both pools' codes and scales.
+struct Int8Maps {
+    CUtensorMap k, v, ks, vs;
+};
 
 __device__ __forceinline__ uint32_t hsub2_1152(uint32_t x) {
     uint32_t y;
@@ -86,18 +93,25 @@ struct DecodeInt8Cfg {
     static constexpr int TILE = BU * D;      // one unit-head of K (or V) codes
     static constexpr int STAGE = 2 * TILE;
     static constexpr int STAGES_BYTES = NW * NST * STAGE;
-    static constexpr int SC_OFF = STAGES_BYTES;  // [warp][stage][K, V][BU] scales
+    static constexpr int SC_OFF = STAGES_BYTES;  // [warp][stage][K, V][U] boxes of B scales
+    static constexpr int SC_BOX = 32;            // floats from box to box: a tensor copy's target is 128-byte aligned
+    static constexpr int SC_STAGE = 2 * U * SC_BOX;
+    static constexpr uint32_t TX = STAGE + 2 * BU * 4;  // bytes of a stage
     static constexpr int RED_BYTES = NW * G * (D + 2) * 4;  // the merge reuses the stage buffers
-    static constexpr int SC_END = SC_OFF + NW * NST * 2 * BU * 4;
+    static constexpr int SC_END = SC_OFF + NW * NST * SC_STAGE * 4;
     static constexpr int BT_OFF = SC_END > RED_BYTES ? SC_END : RED_BYTES;
-    static_assert(BU % 16 == 0 && TILE % 1024 == 0 && BT_OFF % 16 == 0, "unit shape");
+    static_assert(B <= 32 && BU % 16 == 0 && TILE % 1024 == 0 && BT_OFF % 16 == 0, "unit shape");
+    static_assert(RED_BYTES <= SC_END, "merge scratch");
     static size_t smem_bytes(int pb) { return 1024 + BT_OFF + static_cast<size_t>(pb) * 4 + 16 + NW * NST * 8; }
 };
 
+#ifndef PKV_INT8_MIN_CTAS
+#define PKV_INT8_MIN_CTAS 1
+#endif
+
 template <typename T, int D, int B, int G, int NST, int NW, int U>
-__global__ void __launch_bounds__(NW * 32) paged_decode_int8_kernel(const DecodeParams p,
-                                                                    const __grid_constant__ CUtensorMap tm_k,
-                                                                    const __grid_constant__ CUtensorMap tm_v) {
+__global__ void __launch_bounds__(NW * 32, PKV_INT8_MIN_CTAS) paged_decode_int8_kernel(const DecodeParams p,
+                                                                    const __grid_constant__ Int8Maps tm) {
     using C = DecodeInt8Cfg<D, B, G, NST, NW, U>;
     constexpr int kThreads = NW * 32;
     constexpr int BU = C::BU;
@@ -126,6 +140,7 @@ __global__ void __launch_bounds__(NW * 32) paged_decode_int8_kernel(const Decode
     const int b0 = part * p.partition_blocks;
     const int nb = max(0, min(nblk - b0, p.partition_blocks));
     const bool direct = nparts == 1;
+    const int end = min(ctx - b0 * B, nb * B);  // keys of the partition; a unit may reach past it
 
     int* bt_s = reinterpret_cast<int*>(smem + C::BT_OFF);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + ((C::BT_OFF + p.partition_blocks * 4 + 15) & ~15));
@@ -134,7 +149,7 @@ __global__ void __launch_bounds__(NW * 32) paged_decode_int8_kernel(const Decode
         int id = bt_row[i];
         if (id < 0 || id >= p.num_blocks) {
             flag_error(PKV_DEVERR_BLOCK_ID);
-            id = -1;
+            id = static_cast<int>(p.num_blocks);  // read as zeros
         }
         bt_s[i] = id;
     }
@@ -148,33 +163,23 @@ __global__ void __launch_bounds__(NW * 32) paged_decode_int8_kernel(const Decode
     const int nu = (nb + U - 1) / U;  // units of the partition
     const int nw = nu > warp ? (nu - warp + NW - 1) / NW : 0;
     uint8_t* wstage = smem + warp * NST * C::STAGE;
-    float* wscale = reinterpret_cast<float*>(smem + C::SC_OFF) + warp * NST * 2 * BU;
+    float* wscale = reinterpret_cast<float*>(smem + C::SC_OFF) + warp * NST * C::SC_STAGE;
     uint64_t* wbar = bars + warp * NST;
     const uint64_t policy = l2_policy_evict_first();
 
     auto issue = [&](int k) {  // lane 0 only
         const int st = k % NST;
         uint8_t* kd = wstage + st * C::STAGE;
-        float* sd = wscale + st * 2 * BU;
-        int ids[U];
-        int good = 0;
+        float* sd = wscale + st * C::SC_STAGE;
+        mbar_arrive_expect_tx(&wbar[st], C::TX);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int bi = (warp + k * NW) * U + i;
-            ids[i] = bi < nb ? bt_s[bi] : -1;
-            good += ids[i] >= 0;
-        }
-        mbar_arrive_expect_tx(&wbar[st], C::STAGE + good * 2 * B * 4);
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int coord = ids[i] >= 0 ? ids[i] : static_cast<int>(p.num_blocks);  // out of range: zero fill
-            tma_load_4d_hint(kd + i * B * D, &tm_k, 0, g, 0, coord, &wbar[st], policy);
-            tma_load_4d_hint(kd + C::TILE + i * B * D, &tm_v, 0, g, 0, coord, &wbar[st], policy);
-            if (ids[i] >= 0) {
-                const int64_t off = ids[i] * p.block_bytes + g * (B * 4);
-                bulk_load(sd + i * B, p.k_scales + off, B * 4, &wbar[st]);
-                bulk_load(sd + BU + i * B, p.v_scales + off, B * 4, &wbar[st]);
-            }
+            const int id = U > 1 && bi >= nb ? static_cast<int>(p.num_blocks) : bt_s[bi];  // beyond the pool: zero fill
+            tma_load_4d_hint(kd + i * B * D, &tm.k, 0, g, 0, id, &wbar[st], policy);
+            tma_load_4d_hint(kd + C::TILE + i * B * D, &tm.v, 0, g, 0, id, &wbar[st], policy);
+            tma_load_3d_hint(sd + i * C::SC_BOX, &tm.ks, 0, g, id, &wbar[st], policy);
+            tma_load_3d_hint(sd + (U + i) * C::SC_BOX, &tm.vs, 0, g, id, &wbar[st], policy);
         }
     };
     // The pools may still be in the writes of a grid this one depends on (the
@@ -196,18 +201,17 @@ __global__ void __launch_bounds__(NW * 32) paged_decode_int8_kernel(const Decode
         const int hq = G == 8 ? col : col >> 1;
         const T* qrow = reinterpret_cast<const T*>(p.query) +
                         (static_cast<int64_t>(s) * p.num_q_heads + static_cast<int64_t>(g) * G + hq) * D;
-        float qv[KP][8];
+        float qv[KP][2][4];
         uint32_t top = 0;
 #pragma unroll
         for (int kp = 0; kp < KP; ++kp) {
-            float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
-            if (hq < G) {
-                load4(qrow + 32 * kp + 4 * (lane & 3), a);
-                load4(qrow + 32 * kp + 16 + 4 * (lane & 3), b);
-            }
-            top = max(top, max(absmax4(a), absmax4(b)));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) qv[kp][i] = a[i], qv[kp][4 + i] = b[i];
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qv[kp][e][i] = 0.f;
+                if (hq < G) load4(qrow + 32 * kp + 16 * e + 4 * (lane & 3), qv[kp][e]);
+                top = max(top, absmax4(qv[kp][e]));
+            }
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -217,20 +221,21 @@ __global__ void __launch_bounds__(NW * 32) paged_decode_int8_kernel(const Decode
         int sum_hi = 0, sum_lo = 0;
 #pragma unroll
         for (int kp = 0; kp < KP; ++kp) {
-            uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int q = min(32639, max(-32639, __float2int_rn(qv[kp][i] * inv)));  // 0 for 0 * inf
-                const int l = static_cast<int8_t>(q & 255), h = (q - l) >> 8;
-                sum_hi += h;
-                sum_lo += l;
-                hi[i / 4] |= static_cast<uint32_t>(h & 255) << (8 * (i & 3));
-                lo[i / 4] |= static_cast<uint32_t>(l & 255) << (8 * (i & 3));
-            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                if constexpr (G == 8) qf[0][kp][e] = hi[e], qf[NQ - 1][kp][e] = lo[e];
-                else qf[0][kp][e] = (col & 1) ? lo[e] : hi[e];
+                // Adding 1.5 * 2^23 + 128 rounds q to an integer and leaves
+                // q + 128 in the sum's low 16 bits: the upper byte is hi, the
+                // lower one lo + 128.  (A zero row has inv = inf: whatever
+                // integers come out, its scale is 0.)
+                uint32_t u[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(fmaf(qv[kp][e][i], inv, 12583040.f));
+                const uint32_t p01 = __byte_perm(u[0], u[1], 0x5140), p23 = __byte_perm(u[2], u[3], 0x5140);
+                const uint32_t lo = __byte_perm(p01, p23, 0x5410) ^ 0x80808080u, hi = __byte_perm(p01, p23, 0x7632);
+                sum_hi = __dp4a(static_cast<int>(hi), 0x01010101, sum_hi);
+                sum_lo = __dp4a(static_cast<int>(lo), 0x01010101, sum_lo);
+                if constexpr (G == 8) qf[0][kp][e] = hi, qf[NQ - 1][kp][e] = lo;
+                else qf[0][kp][e] = (col & 1) ? lo : hi;
             }
         }
 #pragma unroll
@@ -271,16 +276,11 @@ __global__ void __launch_bounds__(NW * 32) paged_decode_int8_kernel(const Decode
         const int st = k % NST;
         const bool ok = mbar_wait_main(&wbar[st], (k / NST) & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
-        const int u0 = (warp + k * NW) * U;  // the unit's first block in the partition
-        // the unit's keys end at the context's or partition's end or at a bad block id
-        int valid = min(BU, ctx - (b0 + u0) * B);
-#pragma unroll
-        for (int i = 1; i < U; ++i)
-            if (u0 + i >= nb || bt_s[u0 + i] < 0) valid = min(valid, i * B);
-        if (bt_s[u0] >= 0) {
+        {
+            const int valid = end - (warp + k * NW) * BU;  // keys of the unit inside the partition, or more
             const uint8_t* Ks = wstage + st * C::STAGE;
             const uint8_t* Vs = Ks + C::TILE;
-            const float* sk = wscale + st * 2 * BU;
+            const float* sk = wscale + st * C::SC_STAGE + (lane >> 2);
             float t[MT][2][NH], iv[MT][2];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -297,18 +297,29 @@ __global__ void __launch_bounds__(NW * 32) paged_decode_int8_kernel(const Decode
                 }
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const int tok = 16 * mt + (lane >> 2) + 8 * r;
-                    const float ks = sk[tok];
-                    const float vs = max_nan(sk[BU + tok], kInt8MinScale);
+                    const int row = 16 * mt + 8 * r;  // + lane / 4
+                    const float ks = sk[row / B * C::SC_BOX + row % B];
+                    const float vs = max_nan(sk[(U + row / B) * C::SC_BOX + row % B], kInt8MinScale);
                     const float lv = lg2_approx(vs);
-                    iv[mt][r] = tok < valid ? rcp_approx(vs) : 0.f;
+                    iv[mt][r] = rcp_approx(vs);
 #pragma unroll
                     for (int h = 0; h < NH; ++h) {
                         const int dot = G == 8 ? 256 * acc[0][2 * r + h] + acc[NQ - 1][2 * r + h]
                                                : 256 * acc[0][2 * r] + acc[0][2 * r + 1];
-                        t[mt][r][h] = tok < valid ? fmaf(static_cast<float>(dot), ks * qsl[h], lv) : -INFINITY;
+                        t[mt][r][h] = fmaf(static_cast<float>(dot), ks * qsl[h], lv);
                     }
                 }
+            }
+            if (valid < BU) {  // the partition ends in this unit: no weight, whatever the slots hold
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        if (16 * mt + 8 * r + (lane >> 2) >= valid) {
+                            iv[mt][r] = 0.f;
+#pragma unroll
+                            for (int h = 0; h < NH; ++h) t[mt][r][h] = -INFINITY;
+                        }
             }
             // ---- the base moves, and O and the sum are rescaled, only when a
             // unit exceeds it by more than 2^8: weights stay below 256

@@ -143,6 +143,40 @@ int make_int8_map(CUtensorMap* map, const void* pool, int64_t num_blocks, int bl
     return PKV_OK;
 }
 
+// The scales of an int8 pool, float [num_blocks][num_kv_heads, block_size]
+// behind each block's codes: one box = one block x one KV head.
+int make_int8_scale_map(CUtensorMap* map, const void* pool, int64_t num_blocks, int block_size, int num_kv_heads,
+                        int head_dim) {
+    auto fn = encode_fn();
+    if (!fn) {
+        snprintf(g_last_cuda_error, sizeof g_last_cuda_error, "cuTensorMapEncodeTiled unavailable");
+        return PKV_ECUDA;
+    }
+    const uint8_t* scales = static_cast<const uint8_t*>(pool) + (int64_t)block_size * num_kv_heads * head_dim;
+    cuuint64_t dims[3] = {(cuuint64_t)block_size, (cuuint64_t)num_kv_heads, (cuuint64_t)num_blocks};
+    cuuint64_t strides[2] = {(cuuint64_t)block_size * 4,
+                             (cuuint64_t)pkv::int8_block_bytes(block_size, num_kv_heads, head_dim)};
+    cuuint32_t box[3] = {(cuuint32_t)block_size, 1, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<uint8_t*>(scales), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        snprintf(g_last_cuda_error, sizeof g_last_cuda_error, "cuTensorMapEncodeTiled(scales) failed: %d", (int)r);
+        return PKV_ECUDA;
+    }
+    return PKV_OK;
+}
+
+int make_int8_maps(pkv::Int8Maps* m, const void* key_cache, const void* value_cache, int64_t num_blocks,
+                   int block_size, int num_kv_heads, int head_dim) {
+    int rc = make_int8_map(&m->k, key_cache, num_blocks, block_size, num_kv_heads, head_dim);
+    if (!rc) rc = make_int8_map(&m->v, value_cache, num_blocks, block_size, num_kv_heads, head_dim);
+    if (!rc) rc = make_int8_scale_map(&m->ks, key_cache, num_blocks, block_size, num_kv_heads, head_dim);
+    if (!rc) rc = make_int8_scale_map(&m->vs, value_cache, num_blocks, block_size, num_kv_heads, head_dim);
+    return rc;
+}
+
 // Packed query [tokens, num_q_heads, head_dim] as a 3-D tensor; one box =
 // box_tokens (default 128 / group) tokens x group heads x 128 bytes of head_dim.
 int make_query_map(CUtensorMap* map, const void* q, int dtype, int64_t tokens, int num_q_heads, int head_dim,
@@ -249,9 +283,9 @@ constexpr int pick_stages(int stage_bytes, int warps) {
     return n;
 }
 
-template <typename Kern>
-int launch_decode_kernel(Kern kern, size_t smem, int threads, const pkv::DecodeParams& prm, const CUtensorMap& tk,
-                         const CUtensorMap& tv, int grid, const Launch& ln, size_t* configured) {
+template <typename Kern, typename... Maps>
+int launch_decode_kernel(Kern kern, size_t smem, int threads, int grid, const Launch& ln, size_t* configured,
+                         const pkv::DecodeParams& prm, const Maps&... maps) {
     int dev = 0;
     PKV_CUDA(cudaGetDevice(&dev));
     size_t& have = configured[dev & 63];  // largest dynamic smem size set so far on this device
@@ -259,7 +293,7 @@ int launch_decode_kernel(Kern kern, size_t smem, int threads, const pkv::DecodeP
         PKV_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
         have = smem;
     }
-    return launch_kernel(kern, dim3(grid), dim3(threads), smem, ln, prm, tk, tv);
+    return launch_kernel(kern, dim3(grid), dim3(threads), smem, ln, prm, maps...);
 }
 
 template <typename T, int D, int B, int G>
@@ -282,11 +316,11 @@ int launch_decode(const pkv::DecodeParams& prm, const CUtensorMap& tk, const CUt
 #define PKV_DECODE_MMA_MIN_G 1  // 16-bit types with at least this many heads per KV head use warp MMAs
 #endif
     if constexpr (sizeof(T) == 2 && G >= PKV_DECODE_MMA_MIN_G)
-        return launch_decode_kernel(pkv::paged_decode_mma_kernel<T, D, B, G, NST, NW>, smem, NW * 32, prm, tk, tv,
-                                    grid, ln, configured);
+        return launch_decode_kernel(pkv::paged_decode_mma_kernel<T, D, B, G, NST, NW>, smem, NW * 32, grid, ln,
+                                    configured, prm, tk, tv);
     else
-        return launch_decode_kernel(pkv::paged_decode_kernel<T, D, B, G, NST, NW>, smem, NW * 32, prm, tk, tv,
-                                    grid, ln, configured);
+        return launch_decode_kernel(pkv::paged_decode_kernel<T, D, B, G, NST, NW>, smem, NW * 32, grid, ln,
+                                    configured, prm, tk, tv);
 }
 
 template <typename T, int D, int B>
@@ -345,7 +379,7 @@ int launch_decode_fp8(const pkv::DecodeParams& prm, const CUtensorMap& tk, const
     using C = pkv::DecodeFp8Cfg<B, G, NST, NW, U>;
     static size_t configured[64] = {};
     return launch_decode_kernel(pkv::paged_decode_fp8_kernel<T, B, G, NST, NW, U>, C::smem_bytes(prm.partition_blocks),
-                                NW * 32, prm, tk, tv, grid, ln, configured);
+                                NW * 32, grid, ln, configured, prm, tk, tv);
 }
 
 template <typename T, int B>
@@ -372,36 +406,46 @@ int decode_fp8_by_block(int block_size, int group, const pkv::DecodeParams& prm,
 }
 
 // int8 pools: units of at least 16 tokens, two stages per warp.
+#ifndef PKV_INT8_WARPS
+#define PKV_INT8_WARPS 4
+#endif
+#ifndef PKV_INT8_UNIT_TOKENS
+#define PKV_INT8_UNIT_TOKENS 16
+#endif
+#ifndef PKV_INT8_STAGES
+#define PKV_INT8_STAGES 2
+#endif
+
 template <typename T, int D, int B, int G>
-int launch_decode_int8(const pkv::DecodeParams& prm, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
-                       const Launch& ln) {
-    constexpr int NW = 4, NST = 2;
-    constexpr int U = B < 16 ? 16 / B : 1;
+int launch_decode_int8(const pkv::DecodeParams& prm, const pkv::Int8Maps& tm, int grid, const Launch& ln) {
+    constexpr int NW = PKV_INT8_WARPS;
+    constexpr int U = B < PKV_INT8_UNIT_TOKENS ? PKV_INT8_UNIT_TOKENS / B : 1;
+    constexpr int NST = PKV_INT8_STAGES;
     using C = pkv::DecodeInt8Cfg<D, B, G, NST, NW, U>;
     static size_t configured[64] = {};
     return launch_decode_kernel(pkv::paged_decode_int8_kernel<T, D, B, G, NST, NW, U>,
-                                C::smem_bytes(prm.partition_blocks), NW * 32, prm, tk, tv, grid, ln, configured);
+                                C::smem_bytes(prm.partition_blocks), NW * 32, grid, ln, configured, prm, tm);
 }
 
 template <typename T, int D, int B>
-int decode_int8_by_group(int group, const pkv::DecodeParams& prm, const CUtensorMap& tk, const CUtensorMap& tv,
-                         int grid, const Launch& ln) {
+int decode_int8_by_group(int group, const pkv::DecodeParams& prm, const pkv::Int8Maps& tm, int grid,
+                         const Launch& ln) {
     switch (group) {
-        case 1: return launch_decode_int8<T, D, B, 1>(prm, tk, tv, grid, ln);
-        case 2: return launch_decode_int8<T, D, B, 2>(prm, tk, tv, grid, ln);
-        case 4: return launch_decode_int8<T, D, B, 4>(prm, tk, tv, grid, ln);
-        case 8: return launch_decode_int8<T, D, B, 8>(prm, tk, tv, grid, ln);
+        case 1: return launch_decode_int8<T, D, B, 1>(prm, tm, grid, ln);
+        case 2: return launch_decode_int8<T, D, B, 2>(prm, tm, grid, ln);
+        case 4: return launch_decode_int8<T, D, B, 4>(prm, tm, grid, ln);
+        case 8: return launch_decode_int8<T, D, B, 8>(prm, tm, grid, ln);
         default: return PKV_EUNSUPPORTED;
     }
 }
 
 template <typename T, int D>
-int decode_int8_by_block(int block_size, int group, const pkv::DecodeParams& prm, const CUtensorMap& tk,
-                         const CUtensorMap& tv, int grid, const Launch& ln) {
+int decode_int8_by_block(int block_size, int group, const pkv::DecodeParams& prm, const pkv::Int8Maps& tm,
+                         int grid, const Launch& ln) {
     switch (block_size) {
-        case 8: return decode_int8_by_group<T, D, 8>(group, prm, tk, tv, grid, ln);
-        case 16: return decode_int8_by_group<T, D, 16>(group, prm, tk, tv, grid, ln);
-        case 32: return decode_int8_by_group<T, D, 32>(group, prm, tk, tv, grid, ln);
+        case 8: return decode_int8_by_group<T, D, 8>(group, prm, tm, grid, ln);
+        case 16: return decode_int8_by_group<T, D, 16>(group, prm, tm, grid, ln);
+        case 32: return decode_int8_by_group<T, D, 32>(group, prm, tm, grid, ln);
         default: return PKV_EUNSUPPORTED;
     }
 }
@@ -593,14 +637,15 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
         if (rc) return rc;
     }
 
-    auto make_map = [&](CUtensorMap* map, const void* pool) {
-        return int8 ? make_int8_map(map, pool, num_blocks, block_size, num_kv_heads, head_dim)
-                    : make_pool_map(map, pool, kv_dtype, num_blocks, block_size, num_kv_heads, head_dim);
-    };
     CUtensorMap tk, tv;
-    int rc = make_map(&tk, key_cache);
-    if (rc) return rc;
-    rc = make_map(&tv, value_cache);
+    pkv::Int8Maps tm;
+    int rc;
+    if (int8) {
+        rc = make_int8_maps(&tm, key_cache, value_cache, num_blocks, block_size, num_kv_heads, head_dim);
+    } else {
+        rc = make_pool_map(&tk, key_cache, kv_dtype, num_blocks, block_size, num_kv_heads, head_dim);
+        if (!rc) rc = make_pool_map(&tv, value_cache, kv_dtype, num_blocks, block_size, num_kv_heads, head_dim);
+    }
     if (rc) return rc;
 
     pkv::DecodeParams prm;
@@ -622,17 +667,13 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
     prm.num_blocks = num_blocks;
     prm.partition_blocks = (int)pb;
     prm.num_partitions = (int)parts;
-    const int64_t codes = (int64_t)block_size * num_kv_heads * head_dim;
-    prm.k_scales = int8 ? static_cast<const uint8_t*>(key_cache) + codes : nullptr;
-    prm.v_scales = int8 ? static_cast<const uint8_t*>(value_cache) + codes : nullptr;
-    prm.block_bytes = pkv::int8_block_bytes(block_size, num_kv_heads, head_dim);
 
     const Launch ln{s, pdl};
     if (int8) {
         auto by_dim = [&](auto q) {
             using T = decltype(q);
-            return head_dim == 64 ? decode_int8_by_block<T, 64>(block_size, group, prm, tk, tv, (int)grid, ln)
-                                  : decode_int8_by_block<T, 128>(block_size, group, prm, tk, tv, (int)grid, ln);
+            return head_dim == 64 ? decode_int8_by_block<T, 64>(block_size, group, prm, tm, (int)grid, ln)
+                                  : decode_int8_by_block<T, 128>(block_size, group, prm, tm, (int)grid, ln);
         };
         rc = dtype == PKV_F16 ? by_dim(__half()) : by_dim(__nv_bfloat16());
     } else if (fp8) {
@@ -890,7 +931,7 @@ int pkv_decode_partition_size(int num_seqs, int num_q_heads, int num_kv_heads, i
         // 8 KV heads with 8 query heads each (whose merge moves 8x the
         // partials), are fastest unsplit.
         const int64_t waves = 22 * (int64_t)sm_count();
-        if ((dtype == PKV_FP8_E4M3 || dtype == PKV_INT8) && num_q_heads == num_kv_heads && pairs < waves) {
+        if (dtype == PKV_FP8_E4M3 && num_q_heads == num_kv_heads && pairs < waves) {
             const double per_part = (double)num_kv_heads * total_context_tokens / (double)(waves - pairs / 2);
             return round_ps(std::max<int64_t>((int64_t)std::ceil(per_part), 512));
         }

@@ -23,6 +23,12 @@
 //   warp 9      MMA issue
 //   warps 12-15 converters: staging -> f16 K (two stages) and V (two stages)
 // Every wait is bounded, as in prefill.cuh.
+//
+// Few items.  An item is (pair of query tiles, chunk, KV head); where the launch
+// has few of them, each goes to a cluster of CTAs that share out its key tiles.
+// Their partial O, row maxima and sums meet in shared memory: every CTA merges
+// a share of the rows from all of the cluster's (distributed shared memory), so
+// that no scratch is needed for this either.
 #pragma once
 
 #include "decode_int8.cuh"
@@ -38,6 +44,12 @@ struct PrefillInt8Params {
 };
 
 constexpr int kPrefillInt8Threads = 512;
+#ifndef PKV_PREFILL_WIDEN_UNROLL
+#define PKV_PREFILL_WIDEN_UNROLL 1
+#endif
+#ifndef PKV_PREFILL_CONV_REGS
+#define PKV_PREFILL_CONV_REGS 56
+#endif
 constexpr int kPrefillInt8ConvWarp = 12;   // first of four
 constexpr int kPrefillInt8ConvThreads = 128;
 
@@ -59,7 +71,52 @@ struct PrefillInt8Cfg {
     static constexpr int SMEM = 1024 + BAR_OFF + NBAR * 8;
     static constexpr uint32_t TMEM_COLS = 512, S_COL0 = 0, O_COL0 = 256;
     static_assert(SMEM <= 227 * 1024, "shared memory");
+    // the cluster's merge: O [256][D] in fp32 (16-byte chunks swizzled by row), then (max, sum) per row
+    static constexpr int ML_OFF = 256 * D * 4;
+    static constexpr int W_OFF = ML_OFF + 256 * 8;  // the merge's weights, [128][8]
+    static_assert(W_OFF + 128 * 32 <= KC_OFF, "merge scratch");
 };
+
+// Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// ---- thread-block clusters
+__device__ __forceinline__ int cluster_size() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return static_cast<int>(n);
+}
+__device__ __forceinline__ int cluster_rank() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(n));
+    return static_cast<int>(n);
+}
+// Every thread of every CTA of the cluster, its writes before it visible after it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// This CTA's shared address `a` in the CTA of the given rank.
+__device__ __forceinline__ uint32_t cluster_map(uint32_t a, int rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float2 cluster_ld2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+    return v;
+}
 
 template <int kRegs>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
@@ -111,8 +168,10 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 22);
 
-    const int g = static_cast<int>(blockIdx.x) % p.num_kv_heads;
-    const int item = static_cast<int>(blockIdx.x) / p.num_kv_heads;
+    const int parts = cluster_size(), rank = cluster_rank();
+    const int cluster = static_cast<int>(blockIdx.x) / parts;
+    const int g = cluster % p.num_kv_heads;
+    const int item = cluster / p.num_kv_heads;
     int r, pair;
     if (p.num_chunks <= kLptChunks) {
         if (!prefill_item(p.seq_lens, p.query_start_loc, p.num_chunks, C::TT, p.tile_pairs, item, r, pair)) return;
@@ -128,7 +187,7 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
     const int L = p.seq_lens[r];
     const int c0 = L - n;
     if (n < 0 || c0 < 0 || L > p.max_blocks_per_seq * B || n > 2 * p.tile_pairs * C::TT) {
-        if (tid == 0 && pair == 0 && g == 0) flag_error(PKV_DEVERR_LENGTH);
+        if (tid == 0 && pair == 0 && g == 0 && rank == 0) flag_error(PKV_DEVERR_LENGTH);
         if (n < 0 || c0 < 0 || L > p.max_blocks_per_seq * B) return;
     }
     const int qt0 = 2 * pair;
@@ -136,7 +195,11 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
     const bool has_b = (qt0 + 1) * C::TT < n;
     const int nkt_a = (c0 + min((qt0 + 1) * C::TT, n) - 1) / C::BN + 1;
     const int nkt_b = has_b ? (c0 + min((qt0 + 2) * C::TT, n) - 1) / C::BN + 1 : 0;
-    const int nkt = max(nkt_a, nkt_b);
+    // this CTA's share of the key tiles, [tb, tb + nkt), and how many of it each query tile needs
+    const int all = max(nkt_a, nkt_b);
+    const int tb = rank * all / parts;
+    const int nkt = (rank + 1) * all / parts - tb;
+    const int nka = min(max(nkt_a - tb, 0), nkt), nkb = min(max(nkt_b - tb, 0), nkt);
     const int nblk = (L + B - 1) / B;
     const int32_t* bt_row = p.block_tables + static_cast<int64_t>(r) * p.max_blocks_per_seq;
 
@@ -171,43 +234,43 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
     // theirs to the softmax threads, which hold a row of 128 scores:
     // 256 * 208 + 256 * 48 = 512 * 128.
     if (warp >= 8) {
-        regs_dec<48>();
+        regs_dec<PKV_PREFILL_CONV_REGS>();
         if (warp == kPrefillLoadWarp) {
             // ============================================================ loader (whole warp, lane 0 issues)
             const int lane = tid & 31;
             const bool leader = lane == 0;
             const int per_tile = C::BN / B;  // blocks per key tile (4..16)
             float* scales = reinterpret_cast<float*>(smem + C::SC_OFF);
+            // Block ids of this CTA's key tile j, one per lane; read one tile ahead.
             auto fetch_ids = [&](int j) -> int {
-                const int lb = j * per_tile + lane;
+                const int lb = (tb + j) * per_tile + lane;
                 return (lane < per_tile && lb < nblk) ? bt_row[lb] : -1;
             };
             // The codes of tile j, K (which = 0, with the tile's K and V scales) or
-            // V.  Rows of blocks that are not loaded get the scale 0: zeros.
-            auto load_codes = [&](int which, const CUtensorMap* map, int j, int ids) {
-                uint8_t* dst = smem + (which ? C::VC_OFF : C::KC_OFF);
-                float* ks = scales;
-                float* vs = scales + (1 + (j & 1)) * C::BN;
-                if (which == 0 && lane < per_tile && ids < 0)
-                    for (int i = 0; i < B; ++i) ks[lane * B + i] = vs[lane * B + i] = 0.f;
-                const unsigned good = __ballot_sync(0xffffffffu, lane < per_tile && ids >= 0);
-                if (leader) {
+            // V: lane i copies block i.  Rows of blocks that are not loaded get the
+            // scale 0: zeros.
+            auto load_codes = [&](int which, const CUtensorMap* map, int j, int id) {
+                uint8_t* dst = smem + (which ? C::VC_OFF : C::KC_OFF) + lane * B * D;
+                float* ks = scales + lane * B;
+                float* vs = ks + (1 + (j & 1)) * C::BN;
+                if (which == 0 && lane < per_tile && id < 0)
+                    for (int i = 0; i < B; ++i) ks[i] = vs[i] = 0.f;
+                const unsigned good = __ballot_sync(0xffffffffu, lane < per_tile && id >= 0);
+                if (leader) mbar_arrive_expect_tx(&c_full[which], C::C_BYTES + (which ? 0 : __popc(good) * 2 * B * 4));
+                __syncwarp();
+                if (lane < per_tile) {
                     fence_proxy_async();  // the converters' reads before the next copies
-                    mbar_arrive_expect_tx(&c_full[which], C::C_BYTES + (which ? 0 : __popc(good) * 2 * B * 4));
-                }
-                for (int i = 0; i < per_tile; ++i) {
-                    const int id = __shfl_sync(0xffffffffu, ids, i);
-                    if (!leader) continue;
                     const int coord = id >= 0 ? id : static_cast<int>(p.num_blocks);  // out of range: zero fill
-                    tma_load_4d(dst + i * B * D, map, 0, g, 0, coord, &c_full[which]);
+                    tma_load_4d(dst, map, 0, g, 0, coord, &c_full[which]);
                     if (which == 0 && id >= 0) {
                         const int64_t off = id * prm.block_bytes + g * (B * 4);
-                        bulk_load(ks + i * B, prm.k_scales + off, B * 4, &c_full[0]);
-                        bulk_load(vs + i * B, prm.v_scales + off, B * 4, &c_full[0]);
+                        bulk_load(ks, prm.k_scales + off, B * 4, &c_full[0]);
+                        bulk_load(vs, prm.v_scales + off, B * 4, &c_full[0]);
                     }
                 }
+                __syncwarp();
             };
-            if (leader) {
+            if (leader && nkt > 0) {
                 mbar_arrive_expect_tx(q_full, (has_b ? 2 : 1) * C::Q_BYTES);
                 for (int x = 0; x < (has_b ? 2 : 1); ++x) {
 #pragma unroll
@@ -220,7 +283,7 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
             int loaded_k = 0, loaded_v = 0;
             for (int j = 0; j < nkt; ++j) {
                 const int ids_next = fetch_ids(j + 1);
-                if (lane < per_tile && j * per_tile + lane < nblk && (ids < 0 || ids >= p.num_blocks)) {
+                if (lane < per_tile && (tb + j) * per_tile + lane < nblk && (ids < 0 || ids >= p.num_blocks)) {
                     flag_error(PKV_DEVERR_BLOCK_ID);
                     ids = -1;
                 }
@@ -234,7 +297,7 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
             }
             if (leader) {
                 // wait (bounded) for this warp's last copies before the CTA may exit
-                mbar_wait(q_full, 0);
+                if (nkt > 0) mbar_wait(q_full, 0);
                 if (loaded_k > 0) mbar_wait(&c_full[0], (loaded_k - 1) & 1);
                 if (loaded_v > 0) mbar_wait(&c_full[1], (loaded_v - 1) & 1);
             }
@@ -270,12 +333,12 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
                                     t > 0 || kk > 0);
                     if (last) umma_commit(&o_full[x]);
                 };
-                bool ok = mbar_wait_or_abort(kNarrowQ ? q_ready : q_full, 0, abort_flag) &&
+                bool ok = nkt > 0 && mbar_wait_or_abort(kNarrowQ ? q_ready : q_full, 0, abort_flag) &&
                           mbar_wait_or_abort(&k_full[0], 0, abort_flag);
                 if (ok) {
                     tc_fence_after();
-                    issue_s(0, 0);
-                    if (nkt_b > 0) issue_s(1, 0);
+                    if (nka > 0) issue_s(0, 0);
+                    if (nkb > 0) issue_s(1, 0);
                     umma_commit(&k_free[0]);
                 }
                 for (int t = 0; ok && t < nkt; ++t) {
@@ -283,7 +346,7 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
                     bool k_next = false;
                     ok = mbar_wait_or_abort(&v_full[t & 1], (t >> 1) & 1, abort_flag);
                     for (int x = 0; ok && x < 2; ++x) {
-                        const int nk = x == 0 ? nkt_a : nkt_b;
+                        const int nk = x == 0 ? nka : nkb;
                         if (t >= nk) continue;
                         ok = mbar_wait_or_abort(&p_full[x], t & 1, abort_flag);
                         if (!ok) break;
@@ -310,34 +373,37 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
             // ============================================================ converters
             const int ct = tid - kPrefillInt8ConvWarp * 32;
             const float* scales = reinterpret_cast<const float*>(smem + C::SC_OFF);
-            // Widen the staged codes of key tile j into an f16 tile: 16 codes
-            // (two 16-byte vectors of f16) per step.  Row r of the code tile is
-            // swizzled over D bytes, the f16 tile is D / 64 panels of 128-byte
-            // rows, swizzled over 128 bytes.
+            // Widen the staged codes of key tile j into an f16 tile, a row per
+            // thread.  Row r of the code tile is swizzled over D bytes, the f16
+            // tile is D / 64 panels of 128-byte rows, swizzled over 128 bytes:
+            // eight neighbouring lanes touch eight different 16-byte columns
+            // of either.
             constexpr float kMaxScale = 65504.f / 128.f;
+            const int row = ct, sw = row & 7;
+            const float* vs_of = scales + C::BN + row;  // + (j & 1) * BN
             auto widen = [&](int which, int j, uint8_t* dst) {
                 const uint8_t* src = smem + (which ? C::VC_OFF : C::KC_OFF);
-                constexpr int VR = D / 16;  // 16-code vectors per row
-#pragma unroll 4
-                for (int e = ct; e < C::BN * VR; e += kPrefillInt8ConvThreads) {
-                    const int row = e / VR, ch = e % VR;
+                float s = vs_of[(j & 1) * C::BN];
+                if (which) {
+                    if (!(s <= kMaxScale)) s = 0.f;
+                } else {
+                    const float ks = scales[row];
+                    s = s <= kMaxScale && ks <= kMaxScale ? ks : __uint_as_float(0x7fc00000u);
+                }
+                if ((tb + j) * C::BN + row >= L) s = 0.f;
+                const __half hi = __float2half_rn(s);
+                const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(__float2half_rn(s - __half2float(hi)));
+                const uint32_t sh = *reinterpret_cast<const uint32_t*>(&hi2);
+                const uint32_t sl = *reinterpret_cast<const uint32_t*>(&lo2);
+                uint8_t* out = dst + row * 128;
+constexpr int kUnroll = PKV_PREFILL_WIDEN_UNROLL;
+#pragma unroll kUnroll
+                for (int ch = 0; ch < D / 16; ++ch) {
                     const uint4 u = *reinterpret_cast<const uint4*>(src + int8_chunk<D>(row, ch));
-                    float s = scales[(which ? 1 + (j & 1) : 0) * C::BN + row];
-                    if (which) {
-                        if (!(s <= kMaxScale)) s = 0.f;
-                    } else if (!(scales[(1 + (j & 1)) * C::BN + row] <= kMaxScale) || !(s <= kMaxScale)) {
-                        s = __uint_as_float(0x7fc00000u);
-                    }
-                    if (j * C::BN + row >= L) s = 0.f;
-                    const __half hi = __float2half_rn(s);
-                    const __half lo = __float2half_rn(s - __half2float(hi));
-                    const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(lo);
-                    const uint32_t sh = *reinterpret_cast<const uint32_t*>(&hi2);
-                    const uint32_t sl = *reinterpret_cast<const uint32_t*>(&lo2);
                     const uint2 a = widen_codes4(u.x, sh, sl), b = widen_codes4(u.y, sh, sl);
                     const uint2 c = widen_codes4(u.z, sh, sl), d = widen_codes4(u.w, sh, sl);
-                    uint8_t* panel = dst + (ch / 4) * C::BN * 128 + row * 128;
-                    const int v0 = 2 * (ch % 4), sw = row & 7;
+                    uint8_t* panel = out + (ch / 4) * C::BN * 128;
+                    const int v0 = 2 * (ch % 4);
                     *reinterpret_cast<uint4*>(panel + ((v0 ^ sw) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
                     *reinterpret_cast<uint4*>(panel + (((v0 + 1) ^ sw) << 4)) = make_uint4(c.x, c.y, d.x, d.y);
                 }
@@ -359,15 +425,21 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
                 mbar_arrive(&v_full[st]);
             }
         }
+        if (parts > 1) {  // the other roles' share of the merge's barriers
+            __syncwarp();
+            __syncthreads();
+            cluster_sync();
+            cluster_sync();
+        }
     } else {
-        regs_inc<208>();
+        regs_inc<256 - PKV_PREFILL_CONV_REGS>();
         // ================================================================ softmax: one thread per row
         const int x = warp >> 2;
         const int row = (warp & 3) * 32 + (tid & 31);
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const int tok = (qt0 + x) * C::TT + row / G;
         const int qpos = c0 + tok;
-        const int nk = x == 0 ? nkt_a : nkt_b;
+        const int nk = x == 0 ? nka : nkb;
         const uint32_t ts = tmem + lane_base + C::S_COL0 + 128 * x;
         const uint32_t to = tmem + lane_base + C::O_COL0 + D * x;
         const float sl2 = p.scale_log2;
@@ -375,7 +447,7 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
         float m_used = -INFINITY, lsum = 0.f;
         bool ok = true;
         if constexpr (kNarrowQ) {  // this warpgroup's Q tile to f16, in place
-            ok = __all_sync(0xffffffffu, mbar_wait_or_abort(q_full, 0, abort_flag));
+            ok = nkt > 0 && __all_sync(0xffffffffu, mbar_wait_or_abort(q_full, 0, abort_flag));
             if (ok) {
                 if (x == 0 || has_b) {
                     uint8_t* q = smem + C::Q_OFF + x * C::Q_BYTES;
@@ -410,7 +482,7 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
 #pragma unroll
                 for (int i = 0; i < C::BN; ++i) sv[i] = __uint_as_float(u[i]);
             }
-            const int k0 = j * C::BN;
+            const int k0 = (tb + j) * C::BN;
             const bool all_vis = k0 + C::BN - 1 <= qpos;
             float mrow;
             if (all_vis) {
@@ -478,13 +550,14 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
             tc_fence_before();
             mbar_arrive(&p_full[x]);
         }
-        if (ok && nk > 0) {
-            if (__all_sync(0xffffffffu, mbar_wait_or_abort(&o_full[x], 0, abort_flag))) {
-                tc_fence_after();
+        const bool have = ok && nk > 0 && __all_sync(0xffffffffu, mbar_wait_or_abort(&o_full[x], 0, abort_flag));
+        tc_fence_after();
+        T* out = reinterpret_cast<T*>(p.out);
+        if (parts == 1) {
+            if (have) {
                 const bool live = tok < n && !*abort_flag;
                 const float inv = 1.f / lsum;
-                T* dst = reinterpret_cast<T*>(p.out) +
-                         (static_cast<int64_t>(q0 + tok) * p.num_q_heads + static_cast<int64_t>(g) * G + row % G) * D;
+                T* dst = out + (static_cast<int64_t>(q0 + tok) * p.num_q_heads + static_cast<int64_t>(g) * G + row % G) * D;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     float v[32];
@@ -502,6 +575,77 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
                     }
                 }
             }
+        } else {
+            // ---- the cluster's merge.  Every role of this CTA is done with the
+            // tiles, whose memory takes the partial results: O by rows, and (base,
+            // sum) per row; no key seen: (-inf, 0); given up: a negative sum.
+            __syncthreads();
+            const int r256 = x * 128 + row;
+            if (have) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    float v[32];
+                    tmem_ld32(to + c * 32, v);
+#pragma unroll
+                    for (int d = 0; d < 8; ++d)
+                        *reinterpret_cast<float4*>(smem + r256 * D * 4 + (((c * 8 + d) ^ (row & 7)) << 4)) =
+                            make_float4(v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]);
+                }
+            }
+            *reinterpret_cast<float2*>(smem + C::ML_OFF + r256 * 8) =
+                *abort_flag ? make_float2(0.f, -1.f) : have ? make_float2(m_used, lsum) : make_float2(-INFINITY, 0.f);
+            cluster_sync();
+            // This CTA's rows, rank * 256 / parts and on: a thread per row turns the
+            // parts' bases and sums into their weights, then D / 4 lanes of four
+            // elements to a row add the parts up.
+            float* weights = reinterpret_cast<float*>(smem + C::W_OFF);  // [row][8]
+            const uint32_t base = smem_u32(smem);
+            const int rows = 256 / parts, rr0 = rank * rows;
+            if (tid < rows) {
+                float m[8], l[8], mx = -INFINITY, least = 0.f, sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    m[k] = -INFINITY, l[k] = 0.f;
+                    if (k < parts) {
+                        const float2 ml = cluster_ld2(cluster_map(base + C::ML_OFF + (rr0 + tid) * 8, k));
+                        m[k] = ml.x, l[k] = ml.y;
+                    }
+                    mx = fmaxf(mx, m[k]);
+                    least = fminf(least, l[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    // a base of -inf: nothing seen, or (sum NaN) nothing but NaN
+                    m[k] = m[k] == -INFINITY ? (l[k] == 0.f ? 0.f : 1.f) : ex2_approx(m[k] - mx);
+                    sum = fmaf(l[k], m[k], sum);
+                }
+                const float inv = 1.f / sum;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) weights[tid * 8 + k] = least < 0.f ? -1.f : m[k] * inv;
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");  // the softmax warps
+            constexpr int LPR = D / 4;
+            const int lane_d = tid % LPR;
+#pragma unroll 4
+            for (int i = tid / LPR; i < rows; i += 256 / LPR) {
+                const int rr = rr0 + i;
+                const int rtok = (qt0 + rr / 128) * C::TT + (rr % 128) / G;
+                if (rtok >= n) continue;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                float first = 0.f;
+                for (int k = 0; k < parts; ++k) {
+                    const float w = weights[i * 8 + k];
+                    first = fminf(first, w);
+                    if (w == 0.f) continue;  // that part's O may be unwritten
+                    const float4 v = cluster_ld4(cluster_map(base + rr * D * 4 + ((lane_d ^ (rr & 7)) << 4), k));
+                    o.x = fmaf(v.x, w, o.x), o.y = fmaf(v.y, w, o.y), o.z = fmaf(v.z, w, o.z), o.w = fmaf(v.w, w, o.w);
+                }
+                if (!(first < 0.f)) {
+                    T* dst = out + (static_cast<int64_t>(q0 + rtok) * p.num_q_heads + static_cast<int64_t>(g) * G + rr % G) * D + 4 * lane_d;
+                    *reinterpret_cast<uint2*>(dst) = make_uint2(Elem<T>::pack(o.x, o.y), Elem<T>::pack(o.z, o.w));
+                }
+            }
+            cluster_sync();  // no CTA leaves while another reads its shared memory
         }
     }
     tc_fence_before();

@@ -56,6 +56,59 @@ def test_prefill(case):
     assert bool((out[sum(ns):] == 7.0).all())
 
 
+@pytest.mark.parametrize("case", [
+    # chunks of few rows over long contexts: clusters of 2, 4 and 8 CTAs share the key tiles
+    ("bf16", 128, 32, 8, 2, [5000], [3]),            # 2 items: 8 parts of 5 tiles
+    ("f16", 64, 8, 8, 8, [900, 900, 20], [4, 1, 6]),  # 24 items
+    ("bf16", 128, 16, 32, 8, [3000, 11], [70, 1]),   # parts without a visible key for the short chunk
+    ("f16", 128, 16, 16, 8, [2000] * 5, [2, 3, 4, 5, 6]),
+    ("bf16", 64, 16, 4, 1, [0], [1]),
+    ("f16", 128, 8, 8, 1, [1920], [128]),            # the query tiles end on different key tiles
+    ("bf16", 128, 32, 8, 2, [4096, 0], [1, 700]),
+], ids=lambda c: f"{c[0]}D{c[1]}n{c[6][0]}")
+def test_prefill_few_items(case):
+    dt, D, B, Hq, Hkv, c0, ns = case
+    lens = [a + b for a, b in zip(c0, ns)]
+    kp, vp, bt = make_pools(lens, B, Hkv, D, seed=D + B + Hq)
+    q = torch.randn(sum(ns) + 1, Hq, D, device="cuda").to(DT[dt])
+    out = run(q, kp, vp, bt, ns, lens, D ** -0.5)
+    assert pkv.get_device_error() == 0
+    verify(out, q, kp, vp, bt, ns, lens, D ** -0.5)
+    assert bool((out[sum(ns):] == 7.0).all())
+    # the same rows with a NaN query row and a NaN key row, seen by the last row alone
+    q[0, 0, 0] = float("nan")
+    nan = torch.full((1, Hkv, D), float("nan"), device="cuda")
+    last = lens[0] - 1
+    pkv.reshape_and_cache_int8(nan, torch.ones_like(nan), kp, vp, (bt[0, last // B].long() * B + last % B).view(1))
+    bad = run(q, kp, vp, bt, ns, lens, D ** -0.5)
+    want = torch.zeros(sum(ns), Hq, dtype=torch.bool, device="cuda")
+    want[0, 0] = True
+    want[ns[0] - 1] = True
+    assert torch.equal(torch.isnan(bad[: sum(ns)]).all(-1), want) and torch.equal(torch.isnan(bad[: sum(ns)]).any(-1), want)
+    assert torch.equal(bad[: sum(ns)][~want], out[: sum(ns)][~want])
+
+
+def test_prefill_few_items_bad_tables_and_wait_limit():
+    ns, lens = [5, 2], [3000, 2500]
+    kp, vp, bt = make_pools(lens, 16, 2, 128, seed=9)
+    q = torch.randn(7, 4, 128, device="cuda").half()
+    ref = run(q, kp, vp, bt, ns, lens, 0.1)
+    for col in (0, 100, 187):
+        t = bt.clone()
+        t[0, col] = -7
+        out = run(q, kp, vp, t, ns, lens, 0.1)
+        assert pkv.get_device_error() == pkv._binding.DEVERR_BLOCK_ID
+        assert torch.equal(out[5:], ref[5:])
+    pkv.set_wait_limit_ns(0)
+    try:
+        out = run(q, kp, vp, bt, ns, lens, 0.1)
+        torch.cuda.synchronize()
+        assert pkv.get_device_error() & pkv._binding.DEVERR_TIMEOUT
+    finally:
+        pkv.set_wait_limit_ns(pkv.DEFAULT_WAIT_LIMIT_NS)
+    assert torch.equal(run(q, kp, vp, bt, ns, lens, 0.1), ref) and pkv.get_device_error() == 0
+
+
 def test_prefill_many_chunks():
     """More chunks than the longest-first order takes (64), of different lengths, a bound above the longest."""
     ns = [(5 * i) % 7 for i in range(70)]
