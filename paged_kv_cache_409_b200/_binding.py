@@ -154,7 +154,7 @@ def load_library():
 
 def _stream(stream) -> int:
     if stream is None:  # the current stream's handle, without building a Stream object around it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(_current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -168,23 +168,27 @@ def _dev(t: torch.Tensor, name: str) -> int:
     return t.data_ptr()
 
 
+_INT32, _INT64, _UINT8, _FLOAT32 = torch.int32, torch.int64, torch.uint8, torch.float32
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
 def _device(t: torch.Tensor, name: str) -> int:
     """Device index of a call's first tensor, which must be the current device."""
     dev = t.get_device()
     if dev < 0:
         _dev(t, name)  # not a CUDA tensor
-    elif dev != torch.cuda.current_device():
+    elif dev != _current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device")
     return dev
 
 
 def _at(t: torch.Tensor, name: str, dev: int) -> int:
     """Pointer of a contiguous tensor on device ``dev``."""
+    if t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the device of the call's other tensors, not on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _code(t: torch.Tensor) -> int:

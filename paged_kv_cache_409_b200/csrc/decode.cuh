@@ -41,6 +41,7 @@ struct DecodeParams {
     int64_t num_blocks;
     int partition_blocks;  // PB
     int num_partitions;    // P (grid extent)
+    int length_shift;      // int8 pools: sequences in order of length, by classes of len >> length_shift; -1: as listed
 };
 
 template <typename T, int D, int B, int G, int NST, int NW>

@@ -41,6 +41,11 @@ __device__ __forceinline__ float lg2_approx(float x) {
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // max that keeps NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
     float y;
@@ -57,18 +62,10 @@ __device__ __forceinline__ void mma_16832_u8s8(int (&c)[4], const uint32_t (&a)[
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, int c0, int c1, int c2,
-                                                 uint64_t* bar, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "l"(policy)
-        : "memory");
-}
-
-// The tensor maps of both pools' codes and scales.
+// The tensor maps of both pools: K codes, V codes, K scales, V scales, all of
+// four dimensions with the coordinates (0, KV head, 0, block).
 struct Int8Maps {
-    CUtensorMap k, v, ks, vs;
+    CUtensorMap m[4];
 };
 
 __device__ __forceinline__ uint32_t hsub2_1152(uint32_t x) {
@@ -102,12 +99,66 @@ struct DecodeInt8Cfg {
     static constexpr int BT_OFF = SC_END > RED_BYTES ? SC_END : RED_BYTES;
     static_assert(B <= 32 && BU % 16 == 0 && TILE % 1024 == 0 && BT_OFF % 16 == 0, "unit shape");
     static_assert(RED_BYTES <= SC_END, "merge scratch");
+    static_assert(U <= 8, "a lane per copy");
     static size_t smem_bytes(int pb) { return 1024 + BT_OFF + static_cast<size_t>(pb) * 4 + 16 + NW * NST * 8; }
 };
 
 #ifndef PKV_INT8_MIN_CTAS
 #define PKV_INT8_MIN_CTAS 1
 #endif
+
+// The sequence that comes r-th when the batch is ordered by length, longest
+// first: lengths fall into 32 classes (len >> shift, shift chosen for the call's
+// bound), sequences of one class keep their order.  Every CTA finds its own: a
+// histogram and a scan give the class, ballots the place in it.  No CTA then
+// starts a long sequence last.
+constexpr int kMaxRankedSeqs = 256;
+
+template <int kThreads>
+__device__ __forceinline__ int sequence_by_length(const int32_t* lens, int n, int shift, int r) {
+    constexpr int kPer = kMaxRankedSeqs / kThreads, kWarps = kThreads / 32;
+    __shared__ int hist[32];
+    __shared__ int hits[kPer * kWarps];
+    __shared__ int found;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int cls[kPer];  // of sequences tid, tid + kThreads, ...
+#pragma unroll
+    for (int m = 0; m < kPer; ++m) {
+        const int i = tid + m * kThreads;
+        cls[m] = i < n ? min(max(lens[i], 0) >> shift, 31) : -1;
+    }
+    if (tid < 32) hist[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < kPer; ++m)
+        if (cls[m] >= 0) atomicAdd(&hist[cls[m]], 1);
+    __syncthreads();
+    const int count = hist[31 - lane];
+    int upto = count;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += v;
+    }
+    const int at = __ffs(__ballot_sync(0xffffffffu, upto > r)) - 1;  // r < n: some lane's count reaches it
+    int k = r - (__shfl_sync(0xffffffffu, upto, at) - __shfl_sync(0xffffffffu, count, at));  // place in the class
+    unsigned mine[kPer];
+#pragma unroll
+    for (int m = 0; m < kPer; ++m) {
+        mine[m] = __ballot_sync(0xffffffffu, cls[m] == 31 - at);
+        if (lane == 0) hits[m * kWarps + warp] = __popc(mine[m]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < kPer; ++m) {
+        int before = 0;
+#pragma unroll
+        for (int j = 0; j < kPer * kWarps; ++j) before += j < m * kWarps + warp ? hits[j] : 0;
+        if ((mine[m] >> lane & 1) && before + __popc(mine[m] & ((1u << lane) - 1)) == k) found = tid + m * kThreads;
+    }
+    __syncthreads();
+    return found;
+}
 
 template <typename T, int D, int B, int G, int NST, int NW, int U>
 __global__ void __launch_bounds__(NW * 32, PKV_INT8_MIN_CTAS) paged_decode_int8_kernel(const DecodeParams p,
@@ -124,12 +175,13 @@ __global__ void __launch_bounds__(NW * 32, PKV_INT8_MIN_CTAS) paged_decode_int8_
     uint8_t* smem = align_1024(smem_raw);
 
     const int per_seq = p.num_partitions * p.num_kv_heads;
-    const int s = blockIdx.x / per_seq;
-    const int rem = blockIdx.x - s * per_seq;
+    const int turn = blockIdx.x / per_seq;
+    const int rem = blockIdx.x - turn * per_seq;
     const int part = rem / p.num_kv_heads;
     const int g = rem - part * p.num_kv_heads;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
+    const int s = p.length_shift < 0 ? turn : sequence_by_length<kThreads>(p.context_lens, p.num_seqs, p.length_shift, turn);
 
     const int ctx_raw = p.context_lens[s];
     const int nblk = decode_seq_blocks(ctx_raw, B, p.max_blocks_per_seq, p.num_partitions * p.partition_blocks,
@@ -167,28 +219,28 @@ __global__ void __launch_bounds__(NW * 32, PKV_INT8_MIN_CTAS) paged_decode_int8_
     uint64_t* wbar = bars + warp * NST;
     const uint64_t policy = l2_policy_evict_first();
 
-    auto issue = [&](int k) {  // lane 0 only
+    // A unit's copies, one per lane: lane 4 i + j takes block i's part j (K codes,
+    // V codes, K scales, V scales).
+    const CUtensorMap* my_map = &tm.m[lane & 3];
+    const int my_block = lane >> 2;
+    uint8_t* my_dst = (lane & 2) ? reinterpret_cast<uint8_t*>(wscale) + ((lane & 1) * U + my_block) * C::SC_BOX * 4
+                                 : wstage + (lane & 1) * C::TILE + my_block * B * D;
+    constexpr int kStageStep[2] = {C::STAGE, C::SC_STAGE * 4};
+    const int my_step = (lane & 2) ? kStageStep[1] : kStageStep[0];
+    auto issue = [&](int k) {  // whole warp
         const int st = k % NST;
-        uint8_t* kd = wstage + st * C::STAGE;
-        float* sd = wscale + st * C::SC_STAGE;
-        mbar_arrive_expect_tx(&wbar[st], C::TX);
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int bi = (warp + k * NW) * U + i;
+        if (lane == 0) mbar_arrive_expect_tx(&wbar[st], C::TX);
+        __syncwarp();
+        if (lane < 4 * U) {
+            const int bi = (warp + k * NW) * U + my_block;
             const int id = U > 1 && bi >= nb ? static_cast<int>(p.num_blocks) : bt_s[bi];  // beyond the pool: zero fill
-            tma_load_4d_hint(kd + i * B * D, &tm.k, 0, g, 0, id, &wbar[st], policy);
-            tma_load_4d_hint(kd + C::TILE + i * B * D, &tm.v, 0, g, 0, id, &wbar[st], policy);
-            tma_load_3d_hint(sd + i * C::SC_BOX, &tm.ks, 0, g, id, &wbar[st], policy);
-            tma_load_3d_hint(sd + (U + i) * C::SC_BOX, &tm.vs, 0, g, id, &wbar[st], policy);
+            tma_load_4d_hint(my_dst + st * my_step, my_map, 0, g, 0, id, &wbar[st], policy);
         }
     };
     // The pools may still be in the writes of a grid this one depends on (the
     // append of a decode step): their loads start after it completes.
     griddep_wait();
-    if (lane == 0) {
-        for (int k = 0; k < NST && k < nw; ++k) issue(k);
-    }
-    __syncwarp();
+    for (int k = 0; k < NST && k < nw; ++k) issue(k);
 
     // ---- the query as integers, while the first stages are in flight.  B
     // fragment column n = lane / 4 holds dims 32 kp + 4 (lane % 4) + {0..3} and
@@ -387,7 +439,7 @@ __global__ void __launch_bounds__(NW * 32, PKV_INT8_MIN_CTAS) paged_decode_int8_
             }
         }
         __syncwarp();
-        if (lane == 0 && k + NST < nw) {
+        if (k + NST < nw) {
             fence_proxy_async();
             issue(k + NST);
         }

@@ -77,14 +77,6 @@ struct PrefillInt8Cfg {
     static_assert(W_OFF + 128 * 32 <= KC_OFF, "merge scratch");
 };
 
-// Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes).
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
 // ---- thread-block clusters
 __device__ __forceinline__ int cluster_size() {
     uint32_t n;
@@ -246,27 +238,35 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
                 const int lb = (tb + j) * per_tile + lane;
                 return (lane < per_tile && lb < nblk) ? bt_row[lb] : -1;
             };
-            // The codes of tile j, K (which = 0, with the tile's K and V scales) or
-            // V: lane i copies block i.  Rows of blocks that are not loaded get the
-            // scale 0: zeros.
-            auto load_codes = [&](int which, const CUtensorMap* map, int j, int id) {
-                uint8_t* dst = smem + (which ? C::VC_OFF : C::KC_OFF) + lane * B * D;
-                float* ks = scales + lane * B;
-                float* vs = ks + (1 + (j & 1)) * C::BN;
-                if (which == 0 && lane < per_tile && id < 0)
-                    for (int i = 0; i < B; ++i) ks[i] = vs[i] = 0.f;
-                const unsigned good = __ballot_sync(0xffffffffu, lane < per_tile && id >= 0);
-                if (leader) mbar_arrive_expect_tx(&c_full[which], C::C_BYTES + (which ? 0 : __popc(good) * 2 * B * 4));
+            // Ids checked when they arrive; -1: nothing to load.
+            auto checked_ids = [&](int j, int id) -> int {
+                if (lane < per_tile && j < nkt && (tb + j) * per_tile + lane < nblk && (id < 0 || id >= p.num_blocks)) {
+                    flag_error(PKV_DEVERR_BLOCK_ID);
+                    return -1;
+                }
+                return id;
+            };
+            // The tile's scales, four K and four V rows per lane, into registers a
+            // tile ahead of their use (copies of 32 to 128 bytes each would cost as
+            // many bulk copies as the codes); rows of blocks that are not loaded
+            // get 0: zeros.
+            auto fetch_scales = [&](int id, float4& ks, float4& vs) {
+                const int own = __shfl_sync(0xffffffffu, id, 4 * lane / B);
+                ks = vs = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (own >= 0) {
+                    const int64_t off = own * prm.block_bytes + (g * B + (4 * lane) % B) * 4;
+                    ks = *reinterpret_cast<const float4*>(prm.k_scales + off);
+                    vs = *reinterpret_cast<const float4*>(prm.v_scales + off);
+                }
+            };
+            // The codes of a tile, K (0) or V (1): lane i copies block i.
+            auto load_codes = [&](int which, const CUtensorMap* map, int id) {
+                if (leader) mbar_arrive_expect_tx(&c_full[which], C::C_BYTES);
                 __syncwarp();
                 if (lane < per_tile) {
                     fence_proxy_async();  // the converters' reads before the next copies
-                    const int coord = id >= 0 ? id : static_cast<int>(p.num_blocks);  // out of range: zero fill
-                    tma_load_4d(dst, map, 0, g, 0, coord, &c_full[which]);
-                    if (which == 0 && id >= 0) {
-                        const int64_t off = id * prm.block_bytes + g * (B * 4);
-                        bulk_load(ks, prm.k_scales + off, B * 4, &c_full[0]);
-                        bulk_load(vs, prm.v_scales + off, B * 4, &c_full[0]);
-                    }
+                    tma_load_4d(smem + (which ? C::VC_OFF : C::KC_OFF) + lane * B * D, map, 0, g, 0,
+                                id >= 0 ? id : static_cast<int>(p.num_blocks), &c_full[which]);  // out of range: zero fill
                 }
                 __syncwarp();
             };
@@ -279,21 +279,25 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
                                     q0 + (qt0 + x) * C::TT, q_full);
                 }
             }
-            int ids = fetch_ids(0);
+            int ids = checked_ids(0, fetch_ids(0));
+            int ids_next = fetch_ids(1);
+            float4 ks, vs;
+            fetch_scales(ids, ks, vs);
             int loaded_k = 0, loaded_v = 0;
             for (int j = 0; j < nkt; ++j) {
-                const int ids_next = fetch_ids(j + 1);
-                if (lane < per_tile && (tb + j) * per_tile + lane < nblk && (ids < 0 || ids >= p.num_blocks)) {
-                    flag_error(PKV_DEVERR_BLOCK_ID);
-                    ids = -1;
-                }
+                const int ids_later = fetch_ids(j + 2);
                 if (j > 0 && !__all_sync(0xffffffffu, mbar_wait_or_abort_idle(&c_free[0], (j - 1) & 1, abort_flag))) break;
-                load_codes(0, &tm_k, j, ids);
+                *reinterpret_cast<float4*>(scales + 4 * lane) = ks;
+                *reinterpret_cast<float4*>(scales + (1 + (j & 1)) * C::BN + 4 * lane) = vs;
+                __syncwarp();
+                load_codes(0, &tm_k, ids);
                 loaded_k = j + 1;
                 if (j > 0 && !__all_sync(0xffffffffu, mbar_wait_or_abort_idle(&c_free[1], (j - 1) & 1, abort_flag))) break;
-                load_codes(1, &tm_v, j, ids);
+                load_codes(1, &tm_v, ids);
                 loaded_v = j + 1;
-                ids = ids_next;
+                ids = checked_ids(j + 1, ids_next);
+                fetch_scales(ids, ks, vs);
+                ids_next = ids_later;
             }
             if (leader) {
                 // wait (bounded) for this warp's last copies before the CTA may exit

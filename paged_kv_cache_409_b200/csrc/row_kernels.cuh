@@ -40,22 +40,15 @@ __device__ __forceinline__ float int8_scale(uint32_t absmax_bits) {
     return fmaxf(__uint_as_float(absmax_bits) * (1.f / 127.f), kInt8MinScale);
 }
 
-__device__ __forceinline__ float rcp_approx(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// 127 / max |x| within 2^-22 of itself (the hardware reciprocal of max |x| / 128,
-// which keeps the largest floats' inverse normal): one per row instead of a
-// division per element, and a quotient that far off moves a code only when it
-// lies within 127 * 2^-22 of a tie.
+// 127 / max |x|, correctly rounded: one division per row, and a multiplication
+// per element (an approximate reciprocal, 2^-22 off, moved enough codes at ties
+// to raise the error of rows read back in fp16 by half).
 __device__ __forceinline__ float int8_inverse(uint32_t absmax_bits) {
-    return fminf(rcp_approx(__uint_as_float(absmax_bits) * 0.0078125f) * 0.9921875f, kInt8MaxInverse);
+    return fminf(127.f / __uint_as_float(absmax_bits), kInt8MaxInverse);
 }
 
-// Codes of four elements.  x * inv lies in [-127, 127] (up to an error of inv
-// that cannot reach 127.5), and adding 1.5 * 2^23 + 128 in the same FMA
+// Codes of four elements.  x * inv lies in [-127, 127] (up to inv's rounding),
+// and adding 1.5 * 2^23 + 128 in the same FMA
 // rounds the exact product to the nearest integer, ties to even, with the code
 // in the sum's low byte.
 __device__ __forceinline__ uint32_t int8_codes4(const float (&x)[4], float inv) {

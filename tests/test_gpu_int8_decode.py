@@ -152,6 +152,29 @@ def test_decode_long_and_automatic_partitions():
     assert torch.equal(out[0], out[3])
 
 
+@pytest.mark.parametrize("S,Hkv", [(40, 16), (256, 4), (257, 4), (129, 8)])
+def test_decode_batches_taken_by_length(S, Hkv):
+    """More CTAs than run at once: every sequence is taken once, whatever the lengths (all alike, one class, empty
+    and bad ones among them)."""
+    g = torch.Generator().manual_seed(S)
+    for kind in range(3):
+        lens = [torch.randint(0, 200, (S,), generator=g), torch.full((S,), 33),
+                torch.where(torch.rand(S, generator=g) < 0.9, 5, 190)][kind].tolist()
+        kp, vp, bt = make_pools(lens, 16, Hkv, 64, seed=kind)
+        q = torch.randn(S, Hkv, 64, device="cuda").half()
+        for part in (0, 48):
+            out = run(q, kp, vp, bt, lens, 0.125, part)
+            assert pkv.get_device_error() == 0
+            verify(out, q, kp, vp, bt, lens, 0.125, f"kind {kind} partition {part}")
+        cl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        cl[3], cl[7] = -4, 1 << 30  # flagged: an empty row, and a length cut to the table
+        bad = torch.full_like(q, 7.0)
+        pkv.paged_attention_decode_int8(bad, q, kp, vp, bt, cl, 0.125, max(lens), partition_size=0)
+        assert pkv.get_device_error() & pkv._binding.DEVERR_LENGTH
+        keep = [i for i in range(S) if i not in (3, 7)]
+        assert torch.equal(bad[keep], run(q, kp, vp, bt, lens, 0.125, 0)[keep]) and bool((bad[3] == 0).all())
+
+
 def test_step_equals_append_then_decode():
     for B, D, G in ((16, 128, 4), (8, 64, 1)):
         lens = [1, B, 3 * B + 1, 150]

@@ -75,13 +75,14 @@ def reference(x, w, eps, table, pos, interleaved):
 
 
 def check_quantised(x, codes, scales, what=""):
-    """Scales are max |x| * (1 / 127) in fp32, bit for bit; codes are the integers nearest to 127 x / max |x|, where
-    a quotient (up to 127, known within 2^-21 of itself) that close to a tie may go either way."""
+    """Scales are max |x| * (1 / 127) in fp32, codes 128 + the product x * inv, inv = 127 / max |x| rounded to fp32,
+    rounded once (64 bits hold the product): both bit for bit."""
     x = x.numpy().astype(np.float32)
     top = np.abs(x).max(-1)
     assert np.array_equal(scales, np.maximum(top * np.float32(1 / 127), np.float32(2.0 ** -80))), what
-    quotient = x.astype(np.float64) * np.minimum(127 / np.maximum(top.astype(np.float64), 1e-300), 2.0 ** 80)[..., None]
-    assert (np.abs(codes.astype(np.float64) - 128 - quotient) <= 0.5 + 127 * 2.0 ** -21).all(), what
+    with np.errstate(divide="ignore"):
+        inv = np.minimum(np.float32(127) / top, np.float32(2.0 ** 80))
+    assert np.array_equal(codes, 128 + np.rint(x.astype(np.float64) * inv[..., None].astype(np.float64))), what
 
 
 CASES = [
@@ -204,13 +205,13 @@ def test_rotate_into_int8_pools(case, dt):
     ref, size = reference(k, kw, 1e-5, table, pos, interleaved)
     ref, size = ref[live], size[live]
     # the row in fp32 is within 17 * 2^-24 of its pairs' sizes; a scale within that and two roundings; a code within
-    # half a step of a quotient known within 2^-21, and the read value's scale off by two roundings
+    # half a step of a quotient known within 2^-24, and the read value's scale off by two roundings
     slack = 17 * F32 * size.amax(-1)
     s_ref = ref.abs().amax(-1) / 127
     s_got = kscales[at, :, off].double()
     assert bool(((s_got - s_ref).abs() <= slack / 127 + 2 * F32 * s_ref).all())
     value = (kcodes[at, off].double() - 128) * s_got[..., None]
-    assert bool(((value - ref).abs() <= s_got[..., None] * (0.5 + 127 * 2.0 ** -20) + slack[..., None]).all())
+    assert bool(((value - ref).abs() <= s_got[..., None] * (0.5 + 127 * 4 * F32) + slack[..., None]).all())
     # the rest of both pools is as it was
     for got in (kd, vd):
         codes, scales = pkv.int8_pool_views(got.cpu().clone())
