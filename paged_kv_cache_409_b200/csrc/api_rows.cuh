@@ -510,6 +510,7 @@ int pkv_paged_attention_prefill_chunk_int8(void* out, const void* query, const v
     prm.k_scales = static_cast<const uint8_t*>(key_cache) + codes;
     prm.v_scales = static_cast<const uint8_t*>(value_cache) + codes;
     prm.block_bytes = pkv::int8_block_bytes(block_size, num_kv_heads, head_dim);
+    prm.total_q_tokens = (int)total_q_tokens;
     const bool bf16 = dtype == PKV_BF16;
     if (head_dim == 64)
         return bf16 ? prefill_int8_by_group<__nv_bfloat16, 64>(group, prm, tq, tk, tv, (int)items, parts, s)

@@ -41,6 +41,7 @@ struct PrefillInt8Params {
     const uint8_t* k_scales;  // scales of block 0
     const uint8_t* v_scales;
     int64_t block_bytes;
+    int total_q_tokens;
 };
 
 constexpr int kPrefillInt8Threads = 512;
@@ -178,9 +179,11 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
     const int n = p.query_start_loc[r + 1] - q0;
     const int L = p.seq_lens[r];
     const int c0 = L - n;
-    if (n < 0 || c0 < 0 || L > p.max_blocks_per_seq * B || n > 2 * p.tile_pairs * C::TT) {
+    const bool bad = n < 0 || c0 < 0 || q0 < 0 || q0 + static_cast<int64_t>(n) > prm.total_q_tokens ||
+                     L > p.max_blocks_per_seq * B;
+    if (bad || n > 2 * p.tile_pairs * C::TT) {  // the latter is cut to the call's bound
         if (tid == 0 && pair == 0 && g == 0 && rank == 0) flag_error(PKV_DEVERR_LENGTH);
-        if (n < 0 || c0 < 0 || L > p.max_blocks_per_seq * B) return;
+        if (bad) return;
     }
     const int qt0 = 2 * pair;
     if (qt0 * C::TT >= n) return;

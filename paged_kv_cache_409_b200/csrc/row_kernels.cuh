@@ -174,6 +174,9 @@ struct RopeTableParams {
     double turns[128];         // theta_i / pi, in half turns per position
 };
 
+#ifndef PKV_ROPE_MIN_CTAS
+#define PKV_ROPE_MIN_CTAS 7  // resident CTAs per SM the registers must allow
+#endif
 constexpr int kRopeTableRows = 16;
 
 __global__ void __launch_bounds__(128) rope_table_kernel(const __grid_constant__ RopeTableParams p) {
@@ -304,7 +307,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&x)[E], floa
 // row is is known per CTA, and U rows are in flight before the first is used.
 // kPlain: K and V as they are (the append).
 template <typename T, int kPool, int E, int LPR, int U, bool kPlain, bool kNorm, bool kInterleaved>
-__global__ void __launch_bounds__(128) rope_rows_kernel(const RopeRowsParams p) {
+__global__ void __launch_bounds__(128, PKV_ROPE_MIN_CTAS) rope_rows_kernel(const RopeRowsParams p) {
     griddep_launch_dependents();
     constexpr int kPer = 128 / LPR;
     const int sub = threadIdx.x % LPR, rs = threadIdx.x / LPR;

@@ -171,6 +171,25 @@ def test_prefill_bad_tables_are_flagged():
         assert torch.equal(out[:64], ref[:64])
 
 
+def test_prefill_bad_chunk_offsets_are_flagged():
+    """Offsets that leave the packed query, run backwards or start below it: the chunk is skipped, the others stay."""
+    ns, lens = [20, 30, 10], [60, 30, 90]
+    kp, vp, bt = make_pools(lens, 16, 2, 64, seed=11)
+    q = torch.randn(60, 4, 64, device="cuda").half()
+    ref = run(q, kp, vp, bt, ns, lens, 0.1)
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for offsets, kept in (([0, 20, 50, 61], slice(0, 50)), ([-1, 20, 50, 60], slice(20, 60)), ([0, 20, 10, 20], slice(0, 20))):
+        out = torch.full_like(q, 7.0)
+        pkv.paged_attention_prefill_chunk_int8(out, q, kp, vp, bt, sl, torch.tensor(offsets, dtype=torch.int32, device="cuda"),
+                                               32, 0.1)
+        assert pkv.get_device_error() == pkv._binding.DEVERR_LENGTH
+        if offsets != [0, 20, 10, 20]:
+            assert torch.equal(out[kept], ref[kept])
+            rest = torch.ones(60, dtype=torch.bool, device="cuda")
+            rest[kept] = False
+            assert bool((out[rest] == 7.0).all())
+
+
 def test_prefill_row_of_one_equals_decode_closely_and_repeats():
     """Chunks of one row are decode; the same call twice gives the same bits, on two streams at once too."""
     lens = [513, 100, 1]
