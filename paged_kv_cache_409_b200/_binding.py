@@ -564,55 +564,87 @@ def rope_table(cos_sin, base=10000.0, first_position=0, scaling="none", factor=1
     return cos_sin
 
 
-def _head_rows(t: torch.Tensor, name: str, dev: int, T: int, H: int, D: int):
-    """(pointer, elements between tokens) of ``[T, H, D]`` rows whose heads are contiguous within a token, as in a
-    slice of a projection's output."""
-    if t.shape != (T, H, D):
-        raise ValueError(f"{name} must be [{T}, {H}, {D}]: [tokens, heads, head_dim] of the query's tokens and the pools")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on the device of the call's other tensors, not on {t.device}")
-    token, head, element = t.stride()
-    if element != 1 and D > 1 or head != D and H > 1:
-        raise ValueError(f"{name}'s heads must be contiguous within a token")
-    return t.data_ptr(), token if T > 1 else H * D
-
-
-def _rope_and_cache(name, query_out, query, key, value, cos_sin, positions, dev, pools, pool_shape, slot_mapping,
-                    interleaved, q_norm_weight, k_norm_weight, eps, scales, stream):
+# The calls below sit between a layer's kernels, where a few microseconds of host time count: what holds of correct
+# arguments is tested in one expression, and only a call that fails it looks for the reason.
+def _rope_refusal(query_out, query, key, value, cos_sin, positions, dev, pool_shape, slot_mapping, weights):
     T, Hq, D = query.shape
     NB, B, Hkv, Dp = pool_shape
-    dtype = query.dtype
     if Dp != D or query_out.shape != query.shape:
-        raise ValueError("query and query_out must be [tokens, num_q_heads, head_dim] of the pools")
-    if query_out.dtype != dtype or key.dtype != dtype or value.dtype != dtype:
-        raise ValueError("query_out, query, key and value must have one dtype")
+        return "query and query_out must be [tokens, num_q_heads, head_dim] of the pools"
+    if key.shape != (T, Hkv, D) or value.shape != (T, Hkv, D):
+        return "key and value must be [tokens, num_kv_heads, head_dim] of the query's tokens and the pools"
+    if not query_out.dtype == query.dtype == key.dtype == value.dtype:
+        return "query_out, query, key and value must have one dtype"
     if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
-        raise ValueError("slot_mapping must be int64 [tokens]")
-    rotary_dim = max_position = 0
-    table = pos = qw = kw = None
+        return "slot_mapping must be int64 [tokens]"
     if cos_sin is not None:
         if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
-            raise ValueError("cos_sin must be a float32 [positions, rotary_dim] tensor")
+            return "cos_sin must be a float32 [positions, rotary_dim] tensor"
         if positions is None or positions.dtype != torch.int64 or positions.shape != (T,):
-            raise ValueError("positions must be int64 [tokens]")
-        max_position, rotary_dim = cos_sin.shape
-        table, pos = _at(cos_sin, "cos_sin", dev), _at(positions, "positions", dev)
-    if q_norm_weight is not None:
-        if q_norm_weight.dtype != dtype or q_norm_weight.shape != (D,):
-            raise ValueError("q_norm_weight must be [head_dim] in the query's dtype")
-        qw = _at(q_norm_weight, "q_norm_weight", dev)
-    if k_norm_weight is not None:
-        if k_norm_weight.dtype != dtype or k_norm_weight.shape != (D,):
-            raise ValueError("k_norm_weight must be [head_dim] in the query's dtype")
-        kw = _at(k_norm_weight, "k_norm_weight", dev)
-    q, qs = _head_rows(query, "query", dev, T, Hq, D)
-    k, ks = _head_rows(key, "key", dev, T, Hkv, D)
-    v, vs = _head_rows(value, "value", dev, T, Hkv, D)
-    rc = getattr(_lib or load_library(), "pkv_" + name)(
-        _at(query_out, "query_out", dev), q, k, v, qs, ks, vs, qw, kw, eps, table, max_position, rotary_dim,
-        1 if interleaved else 0, pos, pools[0], pools[1], _at(slot_mapping, "slot_mapping", dev), T, Hq, Hkv, D, B, NB,
-        _code(query), *scales, _stream(stream))
-    _ok(rc, name)
+            return "positions must be int64 [tokens]"
+    for w in weights:
+        if w is not None and (w.dtype != query.dtype or w.shape != (D,)):
+            return "a norm weight must be [head_dim] in the query's dtype"
+    for name, t in (("query_out", query_out), ("query", query), ("key", key), ("value", value), ("cos_sin", cos_sin),
+                    ("positions", positions), ("slot_mapping", slot_mapping), ("q_norm_weight", weights[0]),
+                    ("k_norm_weight", weights[1])):
+        if t is None or name == "positions" and cos_sin is None:
+            continue
+        if t.get_device() != dev:
+            return f"{name} must be on the device of the call's other tensors, not on {t.device}"
+        if name in ("query", "key", "value"):
+            if T and (t.stride(2) != 1 or t.stride(1) != D and t.shape[1] > 1):
+                return f"{name}'s heads must be contiguous within a token"
+        elif not t.is_contiguous():
+            return f"{name} must be contiguous"
+    return None
+
+
+def _rope_and_cache(fn, query_out, query, key, value, cos_sin, positions, dev, kc, vc, pool_shape, slot_mapping, interleaved,
+                    qw, kw, eps, scales, stream):
+    shape = query.shape
+    dtype = query.dtype
+    T, Hq, D = shape
+    NB, B, Hkv, Dp = pool_shape
+    rows = (T, Hkv, D)
+    qs, qh, qe = query.stride()
+    ks, kh, ke = key.stride()
+    vs, vh, ve = value.stride()
+    max_position = rotary_dim = 0
+    table = pos = None
+    fine = (Dp == D and query_out.shape == shape and key.shape == rows and value.shape == rows
+            and query_out.dtype == dtype and key.dtype == dtype and value.dtype == dtype
+            and slot_mapping.dtype == _INT64 and slot_mapping.shape == (T,)
+            and qe == 1 and ke == 1 and ve == 1 and (qh == D or Hq == 1) and (kh == D and vh == D or Hkv == 1)
+            and query_out.get_device() == dev and query.get_device() == dev and key.get_device() == dev
+            and value.get_device() == dev and slot_mapping.get_device() == dev
+            and query_out.is_contiguous() and slot_mapping.is_contiguous())
+    if fine and cos_sin is not None:
+        fine = (cos_sin.dtype == _FLOAT32 and cos_sin.dim() == 2 and cos_sin.get_device() == dev and cos_sin.is_contiguous()
+                and positions is not None and positions.dtype == _INT64 and positions.shape == (T,)
+                and positions.get_device() == dev and positions.is_contiguous())
+        if fine:
+            max_position, rotary_dim = cos_sin.shape
+            table, pos = cos_sin.data_ptr(), positions.data_ptr()
+    weights = (qw, kw)
+    if fine and qw is not None:
+        fine = qw.dtype == dtype and qw.shape == (D,) and qw.get_device() == dev and qw.is_contiguous()
+        qw = qw.data_ptr()
+    if fine and kw is not None:
+        fine = kw.dtype == dtype and kw.shape == (D,) and kw.get_device() == dev and kw.is_contiguous()
+        kw = kw.data_ptr()
+    if not fine:
+        why = _rope_refusal(query_out, query, key, value, cos_sin, positions, dev, pool_shape, slot_mapping, weights)
+        if why:
+            raise ValueError(why)
+    if T <= 1:  # a single row's token stride says nothing
+        qs, ks = Hq * D, Hkv * D
+        vs = ks
+    rc = fn(query_out.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(), qs, ks, vs, qw, kw, eps, table,
+            max_position, rotary_dim, 1 if interleaved else 0, pos, kc, vc, slot_mapping.data_ptr(), T, Hq, Hkv, D, B, NB,
+            DTYPE_CODE.get(dtype, -1), *scales, _stream(stream))
+    if rc:
+        raise PagedKVError(fn.__name__[4:], rc)
     return query_out
 
 
@@ -621,12 +653,13 @@ def rope_and_cache(query_out, query, key, value, cos_sin, positions, key_cache, 
     """Norm of every query and key head (weights ``[D]``, or None), rotary positions (rows ``positions`` of
     ``cos_sin``, or None) and the append, in one pass: queries ``[T, Hq, D]`` to ``query_out``, keys and values
     ``[T, Hkv, D]`` to the pools' slots.  Query, key and value may be slices of one projection's output."""
-    if key_cache.dtype != query.dtype or value_cache.dtype != query.dtype or key_cache.shape != value_cache.shape:
+    shape = key_cache.shape
+    if key_cache.dtype != query.dtype or value_cache.dtype != query.dtype or value_cache.shape != shape:
         raise ValueError("the pools must have the query's dtype and one shape")
     dev = _device(query, "query")
-    return _rope_and_cache("rope_and_cache", query_out, query, key, value, cos_sin, positions, dev,
-                           (_at(key_cache, "key_cache", dev), _at(value_cache, "value_cache", dev)), key_cache.shape,
-                           slot_mapping, interleaved, q_norm_weight, k_norm_weight, eps, (), stream)
+    return _rope_and_cache((_lib or load_library()).pkv_rope_and_cache, query_out, query, key, value, cos_sin, positions,
+                           dev, _at(key_cache, "key_cache", dev), _at(value_cache, "value_cache", dev), shape, slot_mapping,
+                           interleaved, q_norm_weight, k_norm_weight, eps, (), stream)
 
 
 def rope_and_cache_fp8(query_out, query, key, value, cos_sin, positions, key_cache, value_cache, slot_mapping, k_scale,
@@ -634,19 +667,19 @@ def rope_and_cache_fp8(query_out, query, key, value, cos_sin, positions, key_cac
     """:func:`rope_and_cache` into E4M3 pools."""
     if key_cache.shape != value_cache.shape:
         raise ValueError("the pools must have one shape")
-    return _rope_and_cache("rope_and_cache_fp8", query_out, query, key, value, cos_sin, positions,
-                           _device(query, "query"),
-                           (_fp8_pool(key_cache, "key_cache"), _fp8_pool(value_cache, "value_cache")), key_cache.shape,
-                           slot_mapping, interleaved, q_norm_weight, k_norm_weight, eps,
-                           (float(k_scale), float(v_scale)), stream)
+    return _rope_and_cache((_lib or load_library()).pkv_rope_and_cache_fp8, query_out, query, key, value, cos_sin,
+                           positions, _device(query, "query"), _fp8_pool(key_cache, "key_cache"),
+                           _fp8_pool(value_cache, "value_cache"), key_cache.shape, slot_mapping, interleaved,
+                           q_norm_weight, k_norm_weight, eps, (float(k_scale), float(v_scale)), stream)
 
 
 def rope_and_cache_int8(query_out, query, key, value, cos_sin, positions, key_cache, value_cache, slot_mapping,
                         interleaved=False, q_norm_weight=None, k_norm_weight=None, eps=1e-6, stream=None):
     """:func:`rope_and_cache` into int8 pools."""
     shape, dev, k, v = _int8_pools(key_cache, value_cache)
-    return _rope_and_cache("rope_and_cache_int8", query_out, query, key, value, cos_sin, positions, dev, (k, v), shape,
-                           slot_mapping, interleaved, q_norm_weight, k_norm_weight, eps, (), stream)
+    return _rope_and_cache((_lib or load_library()).pkv_rope_and_cache_int8, query_out, query, key, value, cos_sin,
+                           positions, dev, k, v, shape, slot_mapping, interleaved, q_norm_weight, k_norm_weight, eps, (),
+                           stream)
 
 
 def int8_block_bytes(block_size, num_kv_heads, head_dim) -> int:
@@ -669,7 +702,7 @@ def int8_pool_views(pool):
 def _int8_pools(key_cache, value_cache):
     """((NB, B, Hkv, D), device, key pointer, value pointer) of two int8 pools."""
     shape = key_cache.shape
-    if len(shape) != 4 or shape[3] <= 4 or key_cache.dtype != torch.uint8 or value_cache.dtype != torch.uint8 \
+    if len(shape) != 4 or shape[3] <= 4 or key_cache.dtype != _UINT8 or value_cache.dtype != _UINT8 \
             or value_cache.shape != shape:
         raise ValueError("key_cache and value_cache must be uint8 [blocks, block_size, num_kv_heads, head_dim + 4] "
                          "pools of one shape")
@@ -678,34 +711,30 @@ def _int8_pools(key_cache, value_cache):
     return (NB, B, H, W - 4), dev, _at(key_cache, "key_cache", dev), _at(value_cache, "value_cache", dev)
 
 
+def _int8_rows(fn, key, value, key_cache, value_cache, slot_mapping, stream):
+    (NB, B, H, D), dev, k, v = _int8_pools(key_cache, value_cache)
+    T = slot_mapping.numel()
+    rows, dtype = (T, H, D), key.dtype
+    if slot_mapping.dtype != _INT64:
+        raise ValueError("slot_mapping must be int64")
+    if key.shape != rows or value.shape != rows or value.dtype != dtype:
+        raise ValueError("the rows must be [tokens, num_kv_heads, head_dim] of the pools, in one dtype")
+    rc = fn(_at(key, "the key rows", dev), _at(value, "the value rows", dev), k, v, _at(slot_mapping, "slot_mapping", dev), T,
+            H, D, B, NB, DTYPE_CODE.get(dtype, -1), _stream(stream))
+    if rc:
+        raise PagedKVError(fn.__name__[4:], rc)
+
+
 def reshape_and_cache_int8(key, value, key_cache, value_cache, slot_mapping, stream=None):
     """Quantise ``key``/``value`` ``[T, Hkv, D]`` (fp32/fp16/bf16) row by row into the int8 pools' slots
     ``slot_mapping`` (int64, -1 = skip)."""
-    (NB, B, H, D), dev, k, v = _int8_pools(key_cache, value_cache)
-    T = slot_mapping.numel()
-    if slot_mapping.dtype != torch.int64:
-        raise ValueError("slot_mapping must be int64")
-    if key.shape != (T, H, D) or value.shape != (T, H, D) or key.dtype != value.dtype:
-        raise ValueError("key and value must be [tokens, num_kv_heads, head_dim] of the pools, in one dtype")
-    rc = (_lib or load_library()).pkv_reshape_and_cache_int8(
-        _at(key, "key", dev), _at(value, "value", dev), k, v, _at(slot_mapping, "slot_mapping", dev), T, H, D, B, NB,
-        _code(key), _stream(stream))
-    _ok(rc, "reshape_and_cache_int8")
+    _int8_rows((_lib or load_library()).pkv_reshape_and_cache_int8, key, value, key_cache, value_cache, slot_mapping, stream)
 
 
 def read_cache_int8(key_out, value_out, key_cache, value_cache, slot_mapping, stream=None):
     """The rows of ``slot_mapping``'s slots of two int8 pools as values, into ``key_out``/``value_out``
     ``[T, Hkv, D]`` (fp32/fp16/bf16); the rows of negative slots are left as they were."""
-    (NB, B, H, D), dev, k, v = _int8_pools(key_cache, value_cache)
-    T = slot_mapping.numel()
-    if slot_mapping.dtype != torch.int64:
-        raise ValueError("slot_mapping must be int64")
-    if key_out.shape != (T, H, D) or value_out.shape != (T, H, D) or key_out.dtype != value_out.dtype:
-        raise ValueError("key_out and value_out must be [tokens, num_kv_heads, head_dim] of the pools, in one dtype")
-    rc = (_lib or load_library()).pkv_read_cache_int8(
-        _at(key_out, "key_out", dev), _at(value_out, "value_out", dev), k, v, _at(slot_mapping, "slot_mapping", dev), T, H,
-        D, B, NB, _code(key_out), _stream(stream))
-    _ok(rc, "read_cache_int8")
+    _int8_rows((_lib or load_library()).pkv_read_cache_int8, key_out, value_out, key_cache, value_cache, slot_mapping, stream)
     return key_out, value_out
 
 
@@ -714,19 +743,26 @@ def _int8_decode_args(out, query, key_cache, value_cache, block_tables, context_
     """The arguments shared by the int8 decode and its step: the device, (out, query, pools, tables) pointers, the
     sizes, the partition and the workspace."""
     (NB, B, Hkv, D), dev, k, v = _int8_pools(key_cache, value_cache)
-    S, Hq, Dq = query.shape
-    if Dq != D or out.shape != query.shape or out.dtype != query.dtype:
+    shape, tables = query.shape, block_tables.shape
+    S, Hq, Dq = shape
+    dtype = query.dtype
+    if Dq != D or out.shape != shape or out.dtype != dtype:
         raise ValueError("out and query must be [num_seqs, num_q_heads, head_dim] of the pools, in one dtype")
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+    if block_tables.dtype != _INT32 or context_lens.dtype != _INT32:
         raise ValueError("block_tables and context_lens must be int32")
-    tables = block_tables.shape
     if len(tables) != 2 or tables[0] != S or context_lens.shape != (S,):
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq] and context_lens [num_seqs]")
-    part, ws_ptr, ws_bytes = _decode_workspace(S, Hq, Hkv, D, B, max_context_len, INT8, partition_size, workspace,
-                                               query.device, total_context_tokens)
+    ws_ptr, ws_bytes = None, 0
+    if partition_size is None:
+        partition_size = _lib.pkv_decode_partition_size(S, Hq, Hkv, D, B, max_context_len, total_context_tokens, INT8)
+        if partition_size < 0:
+            raise PagedKVError("decode_partition_size", partition_size)
+    if partition_size:
+        partition_size, ws_ptr, ws_bytes = _decode_workspace(S, Hq, Hkv, D, B, max_context_len, INT8, partition_size,
+                                                             workspace, query.device, total_context_tokens)
     return (dev, (_at(out, "out", dev), _at(query, "query", dev), k, v, _at(block_tables, "block_tables", dev),
                   _at(context_lens, "context_lens", dev)),
-            (S, Hq, Hkv, D, B, tables[1], NB, int(max_context_len), part, _code(query), ws_ptr, ws_bytes))
+            (S, Hq, Hkv, D, B, tables[1], NB, max_context_len, partition_size, DTYPE_CODE.get(dtype, -1), ws_ptr, ws_bytes))
 
 
 def paged_attention_decode_int8(out, query, key_cache, value_cache, block_tables, context_lens, scale,
@@ -734,10 +770,12 @@ def paged_attention_decode_int8(out, query, key_cache, value_cache, block_tables
                                 total_context_tokens=0):
     """Decode attention over int8 pools (uint8 ``[NB, B, Hkv, D + 4]``); ``out``/``query`` ``[S, Hq, D]`` in fp16 or
     bf16, the other arguments as for :func:`paged_attention_decode`."""
-    load_library()
+    lib = _lib or load_library()
     _, ptrs, sizes = _int8_decode_args(out, query, key_cache, value_cache, block_tables, context_lens, max_context_len,
                                        partition_size, workspace, total_context_tokens)
-    _ok(_lib.pkv_paged_attention_decode_int8(*ptrs, scale, *sizes, _stream(stream)), "paged_attention_decode_int8")
+    rc = lib.pkv_paged_attention_decode_int8(*ptrs, scale, *sizes, _stream(stream))
+    if rc:
+        raise PagedKVError("paged_attention_decode_int8", rc)
     return out
 
 

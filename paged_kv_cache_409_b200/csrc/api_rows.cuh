@@ -43,6 +43,16 @@ int rows_int8_check(const void* x, const void* y, const void* key_cache, const v
     return PKV_OK;
 }
 
+// A row kernel, launched as a programmatic dependent of whatever comes before
+// it in the stream: its CTAs are set up while that kernel drains, and the first
+// thing they do is wait for its completion (griddepcontrol.wait).  Only then do
+// they let a dependent of their own (a step's decode) start, so that one never
+// runs beside anything but this kernel.
+template <typename P>
+int launch_after(void (*kern)(P), dim3 grid, cudaStream_t s, const std::remove_const_t<P>& p) {
+    return launch_kernel(kern, grid, dim3(128), 0, Launch{s, true}, p);
+}
+
 int log2_ceil(int64_t n) {
     int k = 0;
     while ((int64_t(1) << k) < n) ++k;
@@ -72,9 +82,7 @@ int launch_rows(pkv::RopeRowsParams p, cudaStream_t s) {
     const int64_t kv_blocks = ceil_div(p.num_kv_heads, (int64_t)(U / 2) << p.kv_shift);
     const int64_t groups = ceil_div(p.num_tokens, kPer >> (kPlain ? p.kv_shift : std::max(p.q_shift, p.kv_shift)));
     const dim3 grid((unsigned)groups, (unsigned)(p.q_blocks + kv_blocks));
-    pkv::rope_rows_kernel<T, kPool, E, LPR, U, kPlain, kNorm, kInterleaved><<<grid, 128, 0, s>>>(p);
-    PKV_CUDA(cudaGetLastError());
-    return PKV_OK;
+    return launch_after(pkv::rope_rows_kernel<T, kPool, E, LPR, U, kPlain, kNorm, kInterleaved>, grid, s, p);
 }
 
 template <typename T, int kPool, bool kNorm, bool kInterleaved>
@@ -117,9 +125,7 @@ int launch_read_u(pkv::ReadRowsParams p, cudaStream_t s) {
     p.shift = std::min(log2_ceil(kPer), log2_ceil(p.num_kv_heads));
     const dim3 grid((unsigned)ceil_div(p.num_tokens, kPer >> p.shift),
                     (unsigned)ceil_div(p.num_kv_heads, (int64_t)(U / 2) << p.shift));
-    pkv::read_int8_kernel<TD, LPR, U><<<grid, 128, 0, s>>>(p);
-    PKV_CUDA(cudaGetLastError());
-    return PKV_OK;
+    return launch_after(pkv::read_int8_kernel<TD, LPR, U>, grid, s, p);
 }
 
 template <typename TD>
@@ -172,12 +178,14 @@ int launch_prefill_int8(const pkv::PrefillInt8Params& prm, const CUtensorMap& tq
     cfg.blockDim = dim3(pkv::kPrefillInt8Threads);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = parts;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     PKV_CUDA(cudaLaunchKernelEx(&cfg, kern, prm, tq, tk, tv));
     PKV_CUDA(cudaGetLastError());
     return PKV_OK;
@@ -306,9 +314,7 @@ int pkv_rope_table(float* cos_sin, int64_t first_position, int64_t num_positions
     }
     const int64_t threads = ceil_div(num_positions, pkv::kRopeTableRows) * p.half;
     const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(threads, 128), 1 << 20);
-    pkv::rope_table_kernel<<<grid, 128, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    PKV_CUDA(cudaGetLastError());
-    return PKV_OK;
+    return launch_after(pkv::rope_table_kernel, dim3(grid), static_cast<cudaStream_t>(stream), p);
 }
 
 int pkv_rope_and_cache(void* query_out, const void* query, const void* key, const void* value, int64_t query_stride,

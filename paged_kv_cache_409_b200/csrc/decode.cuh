@@ -42,6 +42,7 @@ struct DecodeParams {
     int partition_blocks;  // PB
     int num_partitions;    // P (grid extent)
     int length_shift;      // int8 pools: sequences in order of length, by classes of len >> length_shift; -1: as listed
+    int wait_first;        // int8 pools: a dependent launch after any kernel, which may still write tables and query
 };
 
 template <typename T, int D, int B, int G, int NST, int NW>

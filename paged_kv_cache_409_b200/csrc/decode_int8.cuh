@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(NW * 32, PKV_INT8_MIN_CTAS) paged_decode_int8_
     constexpr int NQ = G == 8 ? 2 : 1;   // MMAs per step: hi and lo apart, or as columns of one
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_1024(smem_raw);
+    if (p.wait_first) griddep_wait();
 
     const int per_seq = p.num_partitions * p.num_kv_heads;
     const int turn = blockIdx.x / per_seq;

@@ -678,7 +678,11 @@ int decode_impl(void* out, const void* query, const void* key_cache, const void*
         while ((max_context_len >> prm.length_shift) > 31) ++prm.length_shift;
     }
 
-    const Launch ln{s, pdl};
+    // The int8 decode is always a dependent launch; outside a step it waits
+    // for the kernel before it first of all.
+    prm.wait_first = int8 && !pdl;
+
+    const Launch ln{s, pdl || int8};
     if (int8) {
         auto by_dim = [&](auto q) {
             using T = decltype(q);

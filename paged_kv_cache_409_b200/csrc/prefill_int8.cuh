@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 22);
 
+    griddep_wait();  // launched as a dependent of whatever comes before it
     const int parts = cluster_size(), rank = cluster_rank();
     const int cluster = static_cast<int>(blockIdx.x) / parts;
     const int g = cluster % p.num_kv_heads;

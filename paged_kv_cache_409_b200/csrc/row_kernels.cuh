@@ -180,6 +180,8 @@ struct RopeTableParams {
 constexpr int kRopeTableRows = 16;
 
 __global__ void __launch_bounds__(128) rope_table_kernel(const __grid_constant__ RopeTableParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
     const int64_t runs = (p.count + kRopeTableRows - 1) / kRopeTableRows;
     for (int64_t e = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; e < runs * p.half;
          e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
@@ -308,6 +310,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&x)[E], floa
 // kPlain: K and V as they are (the append).
 template <typename T, int kPool, int E, int LPR, int U, bool kPlain, bool kNorm, bool kInterleaved>
 __global__ void __launch_bounds__(128, PKV_ROPE_MIN_CTAS) rope_rows_kernel(const RopeRowsParams p) {
+    griddep_wait();  // before the first read: see launch_after
     griddep_launch_dependents();
     constexpr int kPer = 128 / LPR;
     const int sub = threadIdx.x % LPR, rs = threadIdx.x / LPR;
@@ -439,6 +442,8 @@ struct ReadRowsParams {
 // of K and V of one token.
 template <typename TD, int LPR, int U>
 __global__ void __launch_bounds__(128) read_int8_kernel(const ReadRowsParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
     constexpr int kPer = 128 / LPR;
     const int sub = threadIdx.x % LPR, rs = threadIdx.x / LPR;
     const int side = 1 << p.shift;
