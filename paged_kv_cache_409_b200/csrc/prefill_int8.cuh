@@ -49,7 +49,7 @@ constexpr int kPrefillInt8Threads = 512;
 #define PKV_PREFILL_WIDEN_UNROLL 1
 #endif
 #ifndef PKV_PREFILL_CONV_REGS
-#define PKV_PREFILL_CONV_REGS 56
+#define PKV_PREFILL_CONV_REGS 64
 #endif
 constexpr int kPrefillInt8ConvWarp = 12;   // first of four
 constexpr int kPrefillInt8ConvThreads = 128;
@@ -226,9 +226,9 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    // 512 threads launch with 128 registers each; half of them hand 80 of
+    // 512 threads launch with 128 registers each; half of them hand 64 of
     // theirs to the softmax threads, which hold a row of 128 scores:
-    // 256 * 208 + 256 * 48 = 512 * 128.
+    // 256 * 192 + 256 * 64 = 512 * 128.
     if (warp >= 8) {
         regs_dec<PKV_PREFILL_CONV_REGS>();
         if (warp == kPrefillLoadWarp) {
@@ -353,6 +353,7 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
                     const bool next = t + 1 < nkt;
                     bool k_next = false;
                     ok = mbar_wait_or_abort(&v_full[t & 1], (t >> 1) & 1, abort_flag);
+#pragma unroll 1  // one copy of the MMA code for both tiles
                     for (int x = 0; ok && x < 2; ++x) {
                         const int nk = x == 0 ? nka : nkb;
                         if (t >= nk) continue;
@@ -632,25 +633,49 @@ constexpr int kUnroll = PKV_PREFILL_WIDEN_UNROLL;
                 for (int k = 0; k < 8; ++k) weights[tid * 8 + k] = least < 0.f ? -1.f : m[k] * inv;
             }
             asm volatile("bar.sync 1, 256;" ::: "memory");  // the softmax warps
-            constexpr int LPR = D / 4;
+            constexpr int LPR = D / 4, kPass = 256 / LPR, kRows = 4;
             const int lane_d = tid % LPR;
-#pragma unroll 4
-            for (int i = tid / LPR; i < rows; i += 256 / LPR) {
-                const int rr = rr0 + i;
-                const int rtok = (qt0 + rr / 128) * C::TT + (rr % 128) / G;
-                if (rtok >= n) continue;
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                float first = 0.f;
-                for (int k = 0; k < parts; ++k) {
-                    const float w = weights[i * 8 + k];
-                    first = fminf(first, w);
-                    if (w == 0.f) continue;  // that part's O may be unwritten
-                    const float4 v = cluster_ld4(cluster_map(base + rr * D * 4 + ((lane_d ^ (rr & 7)) << 4), k));
-                    o.x = fmaf(v.x, w, o.x), o.y = fmaf(v.y, w, o.y), o.z = fmaf(v.z, w, o.z), o.w = fmaf(v.w, w, o.w);
+            // kRows rows of a thread at once, so that their loads from another
+            // CTA's memory (hundreds of cycles each) are in flight together
+            for (int i0 = tid / LPR; i0 < rows; i0 += kPass * kRows) {
+                float4 o[kRows];
+                float first[kRows];
+                bool live[kRows], any = false;
+#pragma unroll
+                for (int e = 0; e < kRows; ++e) {
+                    const int rr = rr0 + i0 + e * kPass;
+                    live[e] = i0 + e * kPass < rows && (qt0 + rr / 128) * C::TT + (rr % 128) / G < n;
+                    any = any || live[e];
+                    o[e] = make_float4(0.f, 0.f, 0.f, 0.f), first[e] = 0.f;
                 }
-                if (!(first < 0.f)) {
-                    T* dst = out + (static_cast<int64_t>(q0 + rtok) * p.num_q_heads + static_cast<int64_t>(g) * G + rr % G) * D + 4 * lane_d;
-                    *reinterpret_cast<uint2*>(dst) = make_uint2(Elem<T>::pack(o.x, o.y), Elem<T>::pack(o.z, o.w));
+                if (!any) continue;
+#pragma unroll 2
+                for (int k = 0; k < parts; ++k) {
+                    const uint32_t peer = cluster_map(base, k);
+                    float4 v[kRows];
+#pragma unroll
+                    for (int e = 0; e < kRows; ++e) {
+                        const int rr = rr0 + i0 + e * kPass;
+                        if (live[e]) v[e] = cluster_ld4(peer + rr * D * 4 + ((lane_d ^ (rr & 7)) << 4));
+                    }
+#pragma unroll
+                    for (int e = 0; e < kRows; ++e) {
+                        const float w = live[e] ? weights[(i0 + e * kPass) * 8 + k] : 0.f;
+                        first[e] = fminf(first[e], w);
+                        if (w != 0.f) {  // else that part's O may be unwritten
+                            o[e].x = fmaf(v[e].x, w, o[e].x), o[e].y = fmaf(v[e].y, w, o[e].y);
+                            o[e].z = fmaf(v[e].z, w, o[e].z), o[e].w = fmaf(v[e].w, w, o[e].w);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < kRows; ++e) {
+                    const int rr = rr0 + i0 + e * kPass;
+                    const int rtok = (qt0 + rr / 128) * C::TT + (rr % 128) / G;
+                    if (live[e] && !(first[e] < 0.f)) {
+                        T* dst = out + (static_cast<int64_t>(q0 + rtok) * p.num_q_heads + static_cast<int64_t>(g) * G + rr % G) * D + 4 * lane_d;
+                        *reinterpret_cast<uint2*>(dst) = make_uint2(Elem<T>::pack(o[e].x, o[e].y), Elem<T>::pack(o[e].z, o[e].w));
+                    }
                 }
             }
             cluster_sync();  // no CTA leaves while another reads its shared memory
