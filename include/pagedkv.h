@@ -55,8 +55,9 @@ typedef enum { PKV_F32 = 0, PKV_F16 = 1, PKV_BF16 = 2, PKV_FP8_E4M3 = 3 } pkv_dt
  * named *_int8 (and as the dtype of pkv_decode_partition_size).  A row is one
  * token's head_dim elements of one KV head, stored as one-byte codes with a
  * scale of its own, s = max |x| * (1 / 127) in fp32:
- *     u = 128 + round(x * inv),  inv = 127 / max |x| rounded to fp32
- * (to nearest, ties to even), and stands for s * (u - 128).  No calibration is needed: every row uses its
+ *     u = 128 + round(127 x / max |x|)
+ * (the quotient rounded to fp32, then to the nearest integer, ties to even),
+ * and stands for s * (u - 128).  No calibration is needed: every row uses its
  * full range.
  * The bytes of a block are the codes [block_size, num_kv_heads, head_dim] and
  * then the scales, float [num_kv_heads, block_size]:

@@ -5,8 +5,8 @@
 //   read_int8_kernel       the stored rows as values again.
 //
 // Pools of 8-bit rows ("int8 pools").  A row is one token's head_dim elements
-// of one KV head.  Row x is stored as codes u = 128 + rint(x / s), one byte
-// each, and its own fp32 scale s = max |x| / 127; it stands for s * (u - 128).
+// of one KV head.  Row x is stored as codes u = 128 + rint(127 x / max |x|), one
+// byte each, and its own fp32 scale s = max |x| / 127; it stands for s (u - 128).
 // A block's bytes are the codes [block_size, num_kv_heads, head_dim] followed
 // by the scales [num_kv_heads, block_size], so a block stays one contiguous
 // unit that copy_blocks and swap_blocks move whole, its codes have the layout
@@ -40,22 +40,31 @@ __device__ __forceinline__ float int8_scale(uint32_t absmax_bits) {
     return fmaxf(__uint_as_float(absmax_bits) * (1.f / 127.f), kInt8MinScale);
 }
 
-// 127 / max |x|, correctly rounded: one division per row, and a multiplication
-// per element (an approximate reciprocal, 2^-22 off, moved enough codes at ties
-// to raise the error of rows read back in fp16 by half).
-__device__ __forceinline__ float int8_inverse(uint32_t absmax_bits) {
-    return fminf(127.f / __uint_as_float(absmax_bits), kInt8MaxInverse);
+// 127 / max |x| as a sum of two fp32 numbers (the rounded quotient, and what
+// its remainder adds): one division per row, and element times inverse is as
+// exact as a division per element.  With the first part alone, codes of
+// quotients that lie on a tie went astray (rows of fp16 whose largest element
+// is a multiple of 127 steps), and the error of rows read back grew by half.
+struct Int8Inverse {
+    float hi, lo;
+};
+__device__ __forceinline__ Int8Inverse int8_inverse(uint32_t absmax_bits) {
+    const float a = __uint_as_float(absmax_bits), hi = 127.f / a;
+    if (!(hi < kInt8MaxInverse)) return {kInt8MaxInverse, 0.f};
+    return {hi, fmaf(-a, hi, 127.f) * (hi * (1.f / 127.f))};
 }
 
-// Codes of four elements.  x * inv lies in [-127, 127] (up to inv's rounding),
-// and adding 1.5 * 2^23 + 128 in the same FMA
-// rounds the exact product to the nearest integer, ties to even, with the code
-// in the sum's low byte.
-__device__ __forceinline__ uint32_t int8_codes4(const float (&x)[4], float inv) {
-    constexpr float kMagic = 12583040.f;
-    const uint32_t a = __float_as_uint(fmaf(x[0], inv, kMagic)), b = __float_as_uint(fmaf(x[1], inv, kMagic));
-    const uint32_t c = __float_as_uint(fmaf(x[2], inv, kMagic)), d = __float_as_uint(fmaf(x[3], inv, kMagic));
-    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+// Codes of four elements: the quotient rounded to fp32, then to the nearest
+// integer, ties to even, by adding 1.5 * 2^23 + 128, which leaves the code in
+// the sum's low byte.
+__device__ __forceinline__ uint32_t int8_codes4(const float (&x)[4], const Int8Inverse& inv) {
+    const float2 hi = make_float2(inv.hi, inv.hi), lo = make_float2(inv.lo, inv.lo);
+    const float2 magic = make_float2(12583040.f, 12583040.f);
+    const float2 x01 = make_float2(x[0], x[1]), x23 = make_float2(x[2], x[3]);
+    const float2 q01 = __fadd2_rn(__ffma2_rn(x01, hi, __fmul2_rn(x01, lo)), magic);
+    const float2 q23 = __fadd2_rn(__ffma2_rn(x23, hi, __fmul2_rn(x23, lo)), magic);
+    return __byte_perm(__byte_perm(__float_as_uint(q01.x), __float_as_uint(q01.y), 0x0040),
+                       __byte_perm(__float_as_uint(q23.x), __float_as_uint(q23.y), 0x0040), 0x5410);
 }
 
 // Four codes as the integers u - 128, in fp32: a byte over 2^23 is the float
@@ -274,7 +283,7 @@ __device__ __forceinline__ void norm_rotate(float (&x)[E], float (&y)[E], bool n
 }
 
 template <int E>
-__device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[E], float inv) {
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[E], const Int8Inverse& inv) {
     uint32_t w[E / 4];
 #pragma unroll
     for (int i = 0; i < E; i += 4) {
@@ -410,7 +419,7 @@ __global__ void __launch_bounds__(128, PKV_ROPE_MIN_CTAS) rope_rows_kernel(const
                 uint32_t top = max(absmax_bits(x), absmax_bits(y));
 #pragma unroll
                 for (int off = 1; off < LPR; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-                const float inv = int8_inverse(top);
+                const Int8Inverse inv = int8_inverse(top);
                 if (live) {
                     store_codes(dst + a, x, inv);
                     store_codes(dst + b, y, inv);

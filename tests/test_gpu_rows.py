@@ -75,14 +75,15 @@ def reference(x, w, eps, table, pos, interleaved):
 
 
 def check_quantised(x, codes, scales, what=""):
-    """Scales are max |x| * (1 / 127) in fp32, codes 128 + the product x * inv, inv = 127 / max |x| rounded to fp32,
-    rounded once (64 bits hold the product): both bit for bit."""
+    """Scales are max |x| * (1 / 127) in fp32, codes 128 + the quotient 127 x / max |x| rounded to fp32 and then to an
+    integer, ties to even: both bit for bit."""
     x = x.numpy().astype(np.float32)
     top = np.abs(x).max(-1)
     assert np.array_equal(scales, np.maximum(top * np.float32(1 / 127), np.float32(2.0 ** -80))), what
     with np.errstate(divide="ignore"):
-        inv = np.minimum(np.float32(127) / top, np.float32(2.0 ** 80))
-    assert np.array_equal(codes, 128 + np.rint(x.astype(np.float64) * inv[..., None].astype(np.float64))), what
+        inv = np.minimum(127 / top.astype(np.float64), 2.0 ** 80)
+    quotient = (x.astype(np.float64) * inv[..., None]).astype(np.float32)
+    assert np.array_equal(codes, 128 + np.rint(quotient)), what
 
 
 CASES = [
@@ -273,6 +274,11 @@ def test_int8_append_and_read(src, T, Hkv, D, B):
     v[-1, -1] = 0.0
     v[-1, -1, 3] = 127.0               # codes at exact ties: s = 1
     v[-1, -1, 4], v[-1, -1, 5], v[-1, -1, 6] = 2.5, -3.5, 0.5
+    if T > 40:  # scales that are powers of two, and every tie: quotients of n + 1/2
+        k[4:36] = ((torch.arange(32 * Hkv * D) % 254).float() / 2 - 63.25).view(32, Hkv, D).to(dtype)
+        k[4:36, :, 0] = 127.0
+        v[4:36] = (k[4:36].float() * 127 / 64).to(dtype)
+        v[4:36, :, 0] = 127.0 * 127 / 64
     if T > 4:
         k[1, 0, 1] = float("nan")
         v[2, 0, 0] = float("inf")
