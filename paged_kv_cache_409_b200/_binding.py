@@ -557,8 +557,9 @@ def rope_table(cos_sin, base=10000.0, first_position=0, scaling="none", factor=1
     if scaling not in ROPE_SCALING:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}")
     n, rotary_dim = cos_sin.shape
-    spec = RopeSpec(base, factor, alpha, beta, attention_factor, original_max_position, rotary_dim, ROPE_SCALING[scaling])
-    rc = lib.pkv_rope_table(_at(cos_sin, "cos_sin", _device(cos_sin, "cos_sin")), first_position, n, ctypes.byref(spec),
+    spec = RopeSpec(base, factor, alpha, beta, attention_factor, int(original_max_position), rotary_dim,
+                    ROPE_SCALING[scaling])
+    rc = lib.pkv_rope_table(_at(cos_sin, "cos_sin", _device(cos_sin, "cos_sin")), int(first_position), n, ctypes.byref(spec),
                             _stream(stream))
     _ok(rc, "rope_table")
     return cos_sin
@@ -640,7 +641,7 @@ def _rope_and_cache(fn, query_out, query, key, value, cos_sin, positions, dev, k
     if T <= 1:  # a single row's token stride says nothing
         qs, ks = Hq * D, Hkv * D
         vs = ks
-    rc = fn(query_out.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(), qs, ks, vs, qw, kw, eps, table,
+    rc = fn(query_out.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(), qs, ks, vs, qw, kw, float(eps), table,
             max_position, rotary_dim, 1 if interleaved else 0, pos, kc, vc, slot_mapping.data_ptr(), T, Hq, Hkv, D, B, NB,
             DTYPE_CODE.get(dtype, -1), *scales, _stream(stream))
     if rc:
@@ -739,7 +740,7 @@ def read_cache_int8(key_out, value_out, key_cache, value_cache, slot_mapping, st
 
 
 def _int8_decode_args(out, query, key_cache, value_cache, block_tables, context_lens, max_context_len, partition_size,
-                      workspace, total_context_tokens):
+                      workspace, total_context_tokens, stream):
     """The arguments shared by the int8 decode and its step: the device, (out, query, pools, tables) pointers, the
     sizes, the partition and the workspace."""
     (NB, B, Hkv, D), dev, k, v = _int8_pools(key_cache, value_cache)
@@ -752,14 +753,22 @@ def _int8_decode_args(out, query, key_cache, value_cache, block_tables, context_
         raise ValueError("block_tables and context_lens must be int32")
     if len(tables) != 2 or tables[0] != S or context_lens.shape != (S,):
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq] and context_lens [num_seqs]")
+    max_context_len = int(max_context_len)
     ws_ptr, ws_bytes = None, 0
     if partition_size is None:
-        partition_size = _lib.pkv_decode_partition_size(S, Hq, Hkv, D, B, max_context_len, total_context_tokens, INT8)
+        partition_size = _lib.pkv_decode_partition_size(S, Hq, Hkv, D, B, max_context_len, int(total_context_tokens), INT8)
         if partition_size < 0:
             raise PagedKVError("decode_partition_size", partition_size)
     if partition_size:
-        partition_size, ws_ptr, ws_bytes = _decode_workspace(S, Hq, Hkv, D, B, max_context_len, INT8, partition_size,
-                                                             workspace, query.device, total_context_tokens)
+        need = decode_workspace_size(S, Hq, D, max_context_len, partition_size)
+        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+            if stream is None:
+                workspace = torch.empty(need, dtype=_UINT8, device=query.device)
+            else:  # from the pool of the stream that uses it: this one may hand it out again as soon as it is freed
+                with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=query.device)):
+                    workspace = torch.empty(need, dtype=_UINT8, device=query.device)
+        if need:
+            ws_ptr, ws_bytes = _at(workspace, "workspace", dev), workspace.numel() * workspace.element_size()
     return (dev, (_at(out, "out", dev), _at(query, "query", dev), k, v, _at(block_tables, "block_tables", dev),
                   _at(context_lens, "context_lens", dev)),
             (S, Hq, Hkv, D, B, tables[1], NB, max_context_len, partition_size, DTYPE_CODE.get(dtype, -1), ws_ptr, ws_bytes))
@@ -772,8 +781,8 @@ def paged_attention_decode_int8(out, query, key_cache, value_cache, block_tables
     bf16, the other arguments as for :func:`paged_attention_decode`."""
     lib = _lib or load_library()
     _, ptrs, sizes = _int8_decode_args(out, query, key_cache, value_cache, block_tables, context_lens, max_context_len,
-                                       partition_size, workspace, total_context_tokens)
-    rc = lib.pkv_paged_attention_decode_int8(*ptrs, scale, *sizes, _stream(stream))
+                                       partition_size, workspace, total_context_tokens, stream)
+    rc = lib.pkv_paged_attention_decode_int8(*ptrs, float(scale), *sizes, _stream(stream))
     if rc:
         raise PagedKVError("paged_attention_decode_int8", rc)
     return out
@@ -785,7 +794,7 @@ def paged_attention_decode_step_int8(new_keys, new_values, slot_mapping, out, qu
     """The decode step over int8 pools: ``reshape_and_cache_int8`` then ``paged_attention_decode_int8``."""
     load_library()
     dev, ptrs, sizes = _int8_decode_args(out, query, key_cache, value_cache, block_tables, context_lens,
-                                         max_context_len, partition_size, workspace, total_context_tokens)
+                                         max_context_len, partition_size, workspace, total_context_tokens, stream)
     T = slot_mapping.numel()
     rows = (T, sizes[2], sizes[3])
     if slot_mapping.dtype != torch.int64:
@@ -793,7 +802,8 @@ def paged_attention_decode_step_int8(new_keys, new_values, slot_mapping, out, qu
     if new_keys.shape != rows or new_values.shape != rows or not new_keys.dtype == new_values.dtype == query.dtype:
         raise ValueError("new_keys and new_values must be [tokens, num_kv_heads, head_dim] in the query's dtype")
     rc = _lib.pkv_paged_attention_decode_step_int8(_at(new_keys, "new_keys", dev), _at(new_values, "new_values", dev),
-                                                   _at(slot_mapping, "slot_mapping", dev), T, *ptrs, scale, *sizes,
+                                                   _at(slot_mapping, "slot_mapping", dev), T, *ptrs, float(scale),
+                                                   *sizes,
                                                    _stream(stream))
     _ok(rc, "paged_attention_decode_step_int8")
     return out
@@ -815,8 +825,8 @@ def paged_attention_prefill_chunk_int8(out, query, key_cache, value_cache, block
         raise ValueError("block_tables must be [chunks, max_blocks_per_seq] and query_start_loc [chunks + 1]")
     rc = (_lib or load_library()).pkv_paged_attention_prefill_chunk_int8(
         _at(out, "out", dev), _at(query, "query", dev), k, v, _at(block_tables, "block_tables", dev),
-        _at(seq_lens, "seq_lens", dev), _at(query_start_loc, "query_start_loc", dev), R, Tq, max_q_len, scale, Hq, Hkv, D, B,
-        tables[1], NB, _code(query), _stream(stream))
+        _at(seq_lens, "seq_lens", dev), _at(query_start_loc, "query_start_loc", dev), R, Tq, int(max_q_len), float(scale), Hq, Hkv, D,
+        B, tables[1], NB, _code(query), _stream(stream))
     _ok(rc, "paged_attention_prefill_chunk_int8")
     return out
 

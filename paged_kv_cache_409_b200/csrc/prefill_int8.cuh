@@ -242,13 +242,13 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
                 const int lb = (tb + j) * per_tile + lane;
                 return (lane < per_tile && lb < nblk) ? bt_row[lb] : -1;
             };
-            // Ids checked when they arrive; -1: nothing to load.
+            // Ids checked when they arrive; -1: nothing to load (the tiles behind
+            // this CTA's last are another's to check and flag).
             auto checked_ids = [&](int j, int id) -> int {
-                if (lane < per_tile && j < nkt && (tb + j) * per_tile + lane < nblk && (id < 0 || id >= p.num_blocks)) {
-                    flag_error(PKV_DEVERR_BLOCK_ID);
-                    return -1;
-                }
-                return id;
+                if (lane >= per_tile || j >= nkt || (tb + j) * per_tile + lane >= nblk) return -1;
+                if (id >= 0 && id < p.num_blocks) return id;
+                flag_error(PKV_DEVERR_BLOCK_ID);
+                return -1;
             };
             // The tile's scales, four K and four V rows per lane, into registers a
             // tile ahead of their use (copies of 32 to 128 bytes each would cost as

@@ -231,6 +231,14 @@ def test_graph_two_streams_and_shared_inputs():
                 outs.append(call(torch.empty_like(q), torch.empty_like(ws)))
     torch.cuda.synchronize()
     assert all(torch.equal(o, ref) for o in outs)
+    # a stream given by hand, its workspace made by the call
+    st, outs = torch.cuda.Stream(), []
+    for _ in range(10):
+        outs.append(pkv.paged_attention_decode_int8(torch.empty_like(q), q, kp, vp, bt, cl, 0.1, 130, partition_size=32,
+                                                    stream=st))
+        torch.full_like(ws, 255)  # memory that the call has let go of, if it came from this stream's pool
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
     assert pkv.get_device_error() == 0
 
 

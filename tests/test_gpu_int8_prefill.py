@@ -93,9 +93,10 @@ def test_prefill_few_items_bad_tables_and_wait_limit():
     kp, vp, bt = make_pools(lens, 16, 2, 128, seed=9)
     q = torch.randn(7, 4, 128, device="cuda").half()
     ref = run(q, kp, vp, bt, ns, lens, 0.1)
-    for col in (0, 100, 187):
+    # ids of the first and last tiles of the cluster's CTAs, which read a tile ahead
+    for col, bad in ((0, -7), (16, kp.shape[0]), (24, 2**31 - 1), (100, -7), (161, 2**31 - 1), (187, kp.shape[0] + 5)):
         t = bt.clone()
-        t[0, col] = -7
+        t[0, col] = bad
         out = run(q, kp, vp, t, ns, lens, 0.1)
         assert pkv.get_device_error() == pkv._binding.DEVERR_BLOCK_ID
         assert torch.equal(out[5:], ref[5:])
@@ -279,3 +280,75 @@ def test_serving_run():
             ref, bound = reference(qr[i: i + 1], kp, vp, bt[i], n, D ** -0.5, torch.half)
             check(out[i: i + 1], ref, bound, f"step at {n}")
     assert pkv.get_device_error() == 0
+
+
+def test_pools_beyond_four_gib():
+    """Blocks whose bytes lie past 2^32: append, rotation, read, decode and prefill."""
+    NB, B, Hkv, D = 262_000, 16, 8, 128  # 4.4 GB a pool
+    kp, vp = (torch.empty(NB, B, Hkv, D + 4, dtype=torch.uint8, device="cuda") for _ in range(2))
+    L, n = 200, 40
+    ids = torch.arange(NB - 14, NB - 1, device="cuda").flip(0)
+    bt = ids.to(torch.int32).view(1, -1).contiguous()
+    pos = torch.arange(L, device="cuda")
+    slots = ids[pos // B] * B + pos % B
+    k, v = (torch.randn(L, Hkv, D, device="cuda").half() for _ in range(2))
+    pkv.reshape_and_cache_int8(k[:150], v[:150], kp, vp, slots[:150])
+    q = torch.randn(n, 16, D, device="cuda").half()
+    out = torch.empty(50, 16, D, dtype=torch.half, device="cuda")
+    pkv.rope_and_cache_int8(out, torch.cat([q, q[:10]]), k[150:], v[150:], None, None, kp, vp, slots[150:])
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    pkv.read_cache_int8(ko, vo, kp, vp, slots)
+    for x, y in ((k, ko), (v, vo)):
+        assert bool(((x.float() - y.float()).abs() <= x.float().abs().amax(-1, keepdim=True) * (0.51 / 127 + 2.0 ** -10)).all())
+    verify(run(q, kp, vp, bt, [n], [L], 0.09), q, kp, vp, bt, [n], [L], 0.09)
+    dec = torch.empty_like(q[:1])
+    cl = torch.tensor([L], dtype=torch.int32, device="cuda")
+    pkv.paged_attention_decode_int8(dec, q[:1], kp, vp, bt, cl, 0.09, L, partition_size=64)
+    check(dec, *reference(q[:1], kp, vp, bt[0], L, 0.09, torch.half))
+    assert pkv.get_device_error() == 0
+
+
+def test_checked_mode_refuses_bad_tables():
+    """PKV_CHECK=1: the host reads the tables first and launches nothing when one is out of range."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import torch, paged_kv_cache_409_b200 as pkv
+from int8_helpers import make_pools
+kp, vp, bt = make_pools([40, 20], 8, 2, 64, seed=1)
+q = torch.zeros(2, 4, 64, device='cuda').half()
+i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device='cuda')
+i64 = lambda *x: torch.tensor(x, device='cuda')
+k = torch.zeros(2, 2, 64, device='cuda').half()
+table = torch.zeros(50, 32, device='cuda')
+bad = bt.clone()
+bad[1, 0] = kp.shape[0]
+good = [lambda: pkv.paged_attention_decode_int8(q, q, kp, vp, bt, i32(40, 20), 0.1, 40),
+        lambda: pkv.paged_attention_prefill_chunk_int8(q, q, kp, vp, bt, i32(40, 20), i32(0, 1, 2), 1, 0.1),
+        lambda: pkv.reshape_and_cache_int8(k, k, kp, vp, i64(3, -1)), lambda: pkv.read_cache_int8(k, k, kp, vp, i64(3, -1)),
+        lambda: pkv.rope_and_cache_int8(q, q, k, k, table, i64(0, 49), kp, vp, i64(3, 4))]
+wrong = [lambda: pkv.paged_attention_decode_int8(q, q, kp, vp, bad, i32(40, 20), 0.1, 40),
+         lambda: pkv.paged_attention_decode_int8(q, q, kp, vp, bt, i32(41, 20), 0.1, 40),
+         lambda: pkv.paged_attention_prefill_chunk_int8(q, q, kp, vp, bad, i32(40, 20), i32(0, 1, 2), 1, 0.1),
+         lambda: pkv.paged_attention_prefill_chunk_int8(q, q, kp, vp, bt, i32(40, 20), i32(0, 1, 3), 2, 0.1),
+         lambda: pkv.reshape_and_cache_int8(k, k, kp, vp, i64(3, kp.shape[0] * 8)),
+         lambda: pkv.read_cache_int8(k, k, kp, vp, i64(3, kp.shape[0] * 8)),
+         lambda: pkv.rope_and_cache_int8(q, q, k, k, table, i64(0, 50), kp, vp, i64(3, 4)),
+         lambda: pkv.rope_and_cache_int8(q, q, k, k, table, i64(0, 1), kp, vp, i64(3, kp.shape[0] * 8))]
+for f in good:
+    f()
+for n, f in enumerate(wrong):
+    try:
+        f()
+        raise SystemExit(f'call {n} was not refused')
+    except pkv.PagedKVError as e:
+        assert e.status == -3, (n, e.status)
+assert pkv.get_device_error() == 0
+print('refused')
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PKV_CHECK="1", PYTHONPATH=os.pathsep.join([here, os.path.dirname(here)]))
+    r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=200)
+    assert r.returncode == 0 and "refused" in r.stdout, r.stdout + r.stderr
