@@ -440,7 +440,9 @@ size_t pkv_decode_workspace_size(int num_seqs, int num_q_heads, int head_dim, in
  * the GPU and no context is far longer than the mean, else a multiple of
  * block_size.  total_context_tokens (sum of context_lens, 0 = unknown) lets
  * it see a long tail and, for E4M3 pools (dtype PKV_FP8_E4M3) with one query
- * head per KV head, size parts so that the CTAs fill whole waves.  The result
+ * head per KV head, size parts so that the CTAs fill whole waves.  For int8
+ * pools (dtype PKV_INT8, up to 256 sequences) a batch is split where its
+ * longest context is 2.5 times an even share of the work.  The result
  * is at most 4096 * block_size, and a max_context_len above that is always
  * split (into equal parts under the limit), so the decode accepts every
  * recommendation.  num_q_heads must be a multiple of num_kv_heads.  Returns a

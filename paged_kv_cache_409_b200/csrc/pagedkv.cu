@@ -933,9 +933,18 @@ int pkv_decode_partition_size(int num_seqs, int num_q_heads, int num_kv_heads, i
     if (total_context_tokens > 0 && dtype == PKV_INT8 && num_seqs <= pkv::kMaxRankedSeqs) {
         // int8 pools: the decode takes the sequences longest first, so that a
         // split pays only where one sequence alone outlasts its share of the
-        // four CTAs per SM that run at once.
+        // four CTAs per SM that run at once: with the longest context at 1.3,
+        // 1.8, 2.3 shares the whole is faster (156 against 159, 32.0 against
+        // 35, 20.3 against 20.6 us), at 2.7, 3.0, 4.4 the split (89 against
+        // 117, 39 against 48, 70 against 103).  A part of p tokens ends the
+        // call with 10 ns * p, and max / p parts cost 2 to 5 ns of launch each
+        // for every pair, most of them empty: sqrt(pairs * max / 2) tokens,
+        // but no less than 1.5 shares (63 sequences of 512 and one of 4096, 8
+        // KV heads: parts of 512, 1024, 2048 take 34, 27, 31 us; lognormal
+        // lengths up to 8192: parts of 1, 1.5, 2 shares 55, 49, 52).
         const int64_t share = (int64_t)num_kv_heads * total_context_tokens / target;
-        return max_context_len > share + share / 4 ? round_ps(share) : round_ps(longest);
+        if (2 * (int64_t)max_context_len <= 5 * share) return round_ps(longest);
+        return round_ps(std::max(share + share / 2, (int64_t)std::sqrt(0.5 * pairs * max_context_len)));
     }
     if (total_context_tokens > 0) {
         const double mean = (double)total_context_tokens / num_seqs;

@@ -46,6 +46,21 @@ def test_decode(dt, G, B, D):
         verify(out, q, kp, vp, bt, lens, D ** -0.5, f"partition {part}")
 
 
+def test_one_long_sequence_is_split_by_itself():
+    """The recommended partition of a batch with one long context: parts, and the result of the whole."""
+    lens = [40] * 99 + [3001]
+    kp, vp, bt = make_pools(lens, 16, 8, 64, seed=77)
+    q = torch.randn(100, 16, 64, device="cuda").half()
+    part = pkv.decode_partition_size(100, 16, 8, 64, 16, 3001, pkv.INT8, sum(lens))
+    assert 0 < part < 3001 and part % 16 == 0
+    cl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out = pkv.paged_attention_decode_int8(torch.full_like(q, 7.0), q, kp, vp, bt, cl, 0.125, 3001, total_context_tokens=sum(lens))
+    assert pkv.get_device_error() == 0
+    for i in (0, 98, 99):
+        ref, bound = reference(q[i: i + 1], kp, vp, bt[i], lens[i], 0.125, q.dtype)
+        check(out[i: i + 1], ref, bound, f"sequence {i}")
+
+
 @pytest.mark.parametrize("case", [dict(v_size=1e-4), dict(v_size=1e-15), dict(v_size=3e5), dict(k_size=1e-6), dict(k_size=8.0),
                                   dict(v_spread=12), dict(v_spread=30)], ids=str)
 @pytest.mark.parametrize("G", [1, 8])

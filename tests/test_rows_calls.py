@@ -199,10 +199,12 @@ def test_decode_int8_refusals():
     assert dec(step, (P, 0, P, 3)) == EINVAL and dec(step, (P, P, P, -1)) == EINVAL
     assert dec(step, (P, P, P, 0), dt=0) == EUNSUPPORTED
     assert pkv.decode_partition_size(64, 32, 32, 128, 16, 2048, pkv.INT8) == 0
-    # a context is split once it outlasts its share of four CTAs per SM (592 with no device visible) by a quarter
+    # a context is split once it outlasts its share of four CTAs per SM (592 with no device visible) 2.5 times, into
+    # parts of 1.5 shares or sqrt(pairs * max / 2) tokens, whichever is more
     share = 8 * 100000 // 592
-    assert pkv.decode_partition_size(128, 32, 8, 128, 16, share + share // 4, pkv.INT8, 100000) == 0
-    assert pkv.decode_partition_size(128, 32, 8, 128, 16, 4096, pkv.INT8, 100000) == -(-share // 16) * 16
+    assert pkv.decode_partition_size(128, 32, 8, 128, 16, 5 * share // 2, pkv.INT8, 100000) == 0
+    assert pkv.decode_partition_size(128, 32, 8, 128, 16, 4096, pkv.INT8, 100000) == -(-(share + share // 2) // 16) * 16
+    assert pkv.decode_partition_size(64, 64, 8, 128, 16, 4096, pkv.INT8, 63 * 512 + 4096) == 1024
     assert lib.pkv_paged_attention_decode(P, P, P, P, P, P, 0.1, 1, 4, 2, 64, 16, 4, 8, 64, 0, 4, None, 0, None) == -2
 
 
