@@ -59,15 +59,6 @@ int log2_ceil(int64_t n) {
     return k;
 }
 
-#ifndef PKV_ROW_UNROLL
-#define PKV_ROW_UNROLL 4  // rows per thread of a large append or read
-#endif
-// Rows per thread: PKV_ROW_UNROLL keep more bytes in flight once there are
-// enough rows for it, two spread a small batch over the SMs.
-bool many_rows(int64_t tokens, int heads, int per) {
-    return tokens * heads >= (int64_t)per * PKV_ROW_UNROLL * 4 * sm_count();
-}
-
 #ifndef PKV_ROPE_UNROLL
 #define PKV_ROPE_UNROLL 2  // rows per thread of norm + rotation + append
 #endif
@@ -105,11 +96,19 @@ int launch_append_as(const pkv::RopeRowsParams& p, cudaStream_t s) {
     return launch_rows<T, kPool, 8, 16, U, true, false, false>(p, s);
 }
 
+// Rows per thread of the append: K and V of one head, or of two, which keeps
+// more bytes in flight.  Two pay with 16-bit rows, more heads than stand side
+// by side in a CTA (else the second is empty: 8 heads of 128, 16384 tokens: 18
+// against 22 us) and sixteen CTAs per SM (32 heads of 128: 1024 tokens 6.1
+// against 7.0 us, 2048 the same, 16384 65 against 60; fp32, 8191 tokens: 52
+// against 56).
 template <typename T>
 int launch_append_int8(const pkv::RopeRowsParams& p, cudaStream_t s) {
-    return many_rows(p.num_tokens, 2 * p.num_kv_heads, 256 / row_lanes(p.head_dim))
-               ? launch_append_as<T, PKV_ROW_UNROLL>(p, s)
-               : launch_append_as<T, 2>(p, s);
+    const int side = 256 / row_lanes(p.head_dim);
+    const int64_t rows = 2 * p.num_tokens * p.num_kv_heads;
+    if (sizeof(T) == 2 && p.num_kv_heads > side && rows >= (int64_t)side * 4 * 16 * sm_count())
+        return launch_append_as<T, 4>(p, s);
+    return launch_append_as<T, 2>(p, s);
 }
 
 template <typename T, int kPool>
@@ -119,9 +118,9 @@ int launch_rope(const pkv::RopeRowsParams& p, bool interleaved, cudaStream_t s) 
     return interleaved ? launch_rope_as<T, kPool, false, true>(p, s) : launch_rope_as<T, kPool, false, false>(p, s);
 }
 
-template <typename TD, int LPR, int U>
-int launch_read_u(pkv::ReadRowsParams p, cudaStream_t s) {
-    constexpr int kPer = 128 / LPR;
+template <typename TD, int LPR>
+int launch_read_as(pkv::ReadRowsParams p, cudaStream_t s) {
+    constexpr int U = 2, kPer = 128 / LPR;  // four: 5 % faster with 8 heads, 2-25 % slower with 32
     p.shift = std::min(log2_ceil(kPer), log2_ceil(p.num_kv_heads));
     const dim3 grid((unsigned)ceil_div(p.num_tokens, kPer >> p.shift),
                     (unsigned)ceil_div(p.num_kv_heads, (int64_t)(U / 2) << p.shift));
@@ -130,12 +129,10 @@ int launch_read_u(pkv::ReadRowsParams p, cudaStream_t s) {
 
 template <typename TD>
 int launch_read(const pkv::ReadRowsParams& p, cudaStream_t s) {
-    constexpr int U = PKV_ROW_UNROLL;
     const int lanes = row_lanes(p.head_dim) / 2;
-    const bool many = many_rows(p.num_tokens, 2 * p.num_kv_heads, 128 / lanes);
-    if (lanes == 4) return many ? launch_read_u<TD, 4, U>(p, s) : launch_read_u<TD, 4, 2>(p, s);
-    if (lanes == 8) return many ? launch_read_u<TD, 8, U>(p, s) : launch_read_u<TD, 8, 2>(p, s);
-    return many ? launch_read_u<TD, 16, U>(p, s) : launch_read_u<TD, 16, 2>(p, s);
+    if (lanes == 4) return launch_read_as<TD, 4>(p, s);
+    if (lanes == 8) return launch_read_as<TD, 8>(p, s);
+    return launch_read_as<TD, 16>(p, s);
 }
 
 // CTAs that share an item's key tiles (a cluster of 1, 2, 4 or 8).  Measured on
@@ -165,7 +162,7 @@ int launch_prefill_int8(const pkv::PrefillInt8Params& prm, const CUtensorMap& tq
     PKV_CUDA(cudaGetDevice(&dev));
     static bool configured[64] = {};
     if (!configured[dev & 63]) {
-        // the softmax threads' share (208) comes out of what the block is
+        // the softmax threads' share (192) comes out of what the block is
         // launched with: 512 threads x 128 registers, no fewer
         cudaFuncAttributes a;
         PKV_CUDA(cudaFuncGetAttributes(&a, kern));

@@ -29,6 +29,13 @@
 // and the CTA merge are those of decode.cuh; a block's scales (one KV head's)
 // come through tensor maps of their own, with the codes' coordinates and on the
 // same barrier.
+//
+// Bound by memory.  64 sequences of [128, 2048] tokens x 32 heads of 128, fp16:
+// 94 us, 6.35 TB/s (0.97 of a copy).  256 sequences x 8 KV heads, 8 query heads
+// each: 118-124 us, 5.9-6.2 TB/s; there the eight columns of an MMA are all in
+// use, and what is left is the ranking and the last wave.  Four warps of two
+// stages and units of 16 tokens: 8 warps, 2 warps, 3 stages and units of 32 are
+// all slower on the latter (172, 148, 145, 140 us when this version took 130).
 #pragma once
 
 #include "decode.cuh"
@@ -103,10 +110,6 @@ struct DecodeInt8Cfg {
     static size_t smem_bytes(int pb) { return 1024 + BT_OFF + static_cast<size_t>(pb) * 4 + 16 + NW * NST * 8; }
 };
 
-#ifndef PKV_INT8_MIN_CTAS
-#define PKV_INT8_MIN_CTAS 1
-#endif
-
 // The sequence that comes r-th when the batch is ordered by length, longest
 // first: lengths fall into 32 classes (len >> shift, shift chosen for the call's
 // bound), sequences of one class keep their order.  Every CTA finds its own: a
@@ -161,7 +164,7 @@ __device__ __forceinline__ int sequence_by_length(const int32_t* lens, int n, in
 }
 
 template <typename T, int D, int B, int G, int NST, int NW, int U>
-__global__ void __launch_bounds__(NW * 32, PKV_INT8_MIN_CTAS) paged_decode_int8_kernel(const DecodeParams p,
+__global__ void __launch_bounds__(NW * 32) paged_decode_int8_kernel(const DecodeParams p,
                                                                     const __grid_constant__ Int8Maps tm) {
     using C = DecodeInt8Cfg<D, B, G, NST, NW, U>;
     constexpr int kThreads = NW * 32;

@@ -29,6 +29,15 @@
 // Their partial O, row maxima and sums meet in shared memory: every CTA merges
 // a share of the rows from all of the cluster's (distributed shared memory), so
 // that no scratch is needed for this either.
+//
+// Bound by the chain of a query tile's steps (S, softmax, P.V: 2.25 us per 128
+// keys for two tiles, of which the tensor cores work 1.5): four chunks of 512
+// rows over up to 8446 keys, 32 query heads on 8 KV heads of 128, 166 us, 705
+// TFLOP/s (0.43 of the bf16 rate), set by the items of 66 key tiles.  In the
+// chain it is the softmax threads' issue slots and latency that count, not the
+// exponential unit: a polynomial for an eighth, a quarter, half of the
+// exponentials took 170, 180, 194 us, P handed over in two halves 190, scores
+// read again from tensor memory in loops of 32 to 128 columns 179-195.
 #pragma once
 
 #include "decode_int8.cuh"
@@ -46,10 +55,10 @@ struct PrefillInt8Params {
 
 constexpr int kPrefillInt8Threads = 512;
 #ifndef PKV_PREFILL_WIDEN_UNROLL
-#define PKV_PREFILL_WIDEN_UNROLL 1
+#define PKV_PREFILL_WIDEN_UNROLL 1  // 2, 4, 8: slower, the loops compete for the instruction caches
 #endif
 #ifndef PKV_PREFILL_CONV_REGS
-#define PKV_PREFILL_CONV_REGS 64
+#define PKV_PREFILL_CONV_REGS 64  // registers of the second half's threads; the softmax gets 256 minus this
 #endif
 constexpr int kPrefillInt8ConvWarp = 12;   // first of four
 constexpr int kPrefillInt8ConvThreads = 128;
@@ -405,7 +414,7 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
                 const uint32_t sh = *reinterpret_cast<const uint32_t*>(&hi2);
                 const uint32_t sl = *reinterpret_cast<const uint32_t*>(&lo2);
                 uint8_t* out = dst + row * 128;
-constexpr int kUnroll = PKV_PREFILL_WIDEN_UNROLL;
+                constexpr int kUnroll = PKV_PREFILL_WIDEN_UNROLL;
 #pragma unroll kUnroll
                 for (int ch = 0; ch < D / 16; ++ch) {
                     const uint4 u = *reinterpret_cast<const uint4*>(src + int8_chunk<D>(row, ch));

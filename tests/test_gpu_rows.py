@@ -320,6 +320,30 @@ def test_int8_append_and_read(src, T, Hkv, D, B):
             assert bool((o[~ok] == 9.0).all())
 
 
+@pytest.mark.parametrize("T,Hkv,D,B", [(4001, 20, 128, 16), (4099, 40, 64, 32), (3001, 11, 256, 8)])
+def test_int8_append_of_many_rows(T, Hkv, D, B):
+    """Batches and head counts at which a thread of the append takes two heads: the last ones are missing here."""
+    g = torch.Generator().manual_seed(D)
+    k, v = torch.randn(T, Hkv, D, generator=g).half(), torch.randn(T, Hkv, D, generator=g).half()
+    NB = -(-T // B)
+    slots = torch.randperm(NB * B, generator=g)[:T]
+    pools = [torch.full((NB, B, Hkv, D + 4), 77, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    pkv.reshape_and_cache_int8(k.cuda(), v.cuda(), *pools, slots.cuda())
+    assert pkv.get_device_error() == 0
+    rest = torch.ones(NB * B, dtype=torch.bool)
+    rest[slots] = False
+    for x, got in ((k, pools[0].cpu()), (v, pools[1].cpu())):
+        codes, scales = pkv.int8_pool_views(got)
+        check_quantised(x.float(), codes[slots // B, slots % B].numpy(), scales[slots // B, :, slots % B].numpy())
+        assert bool((codes.reshape(-1, Hkv, D)[rest] == 77).all())
+    ko, vo = torch.empty(T, Hkv, D, device="cuda"), torch.empty(T, Hkv, D, device="cuda")
+    pkv.read_cache_int8(ko, vo, *pools, slots.cuda())
+    for o, got in ((ko, pools[0].cpu()), (vo, pools[1].cpu())):
+        codes, scales = pkv.int8_pool_views(got)
+        at, off = slots // B, slots % B
+        assert torch.equal(o.cpu(), (codes[at, off].float() - 128) * scales[at, :, off][..., None])
+
+
 def test_int8_blocks_move_whole():
     """copy_blocks and swap_blocks move an int8 pool's codes and scales together."""
     NB, B, Hkv, D = 6, 16, 2, 64
