@@ -406,12 +406,15 @@ int decode_fp8_by_block(int block_size, int group, const pkv::DecodeParams& prm,
     }
 }
 
-// int8 pools: units of at least 16 tokens, two stages per warp.
+// int8 pools: two stages per warp, each a unit of blocks.  Units have at least
+// 16 tokens; 32 with 64-byte rows, where 16 make only a kilobyte per copy
+// (blocks of 16: 127 -> 103, 136 -> 107, 66 -> 51, 58 -> 57 us for 1, 2, 4, 8
+// query heads per KV head, 128 sequences over [512, 4096]), except with blocks
+// of 8 and few heads, whose units would take 16 copies (118 -> 122, 108 -> 117,
+// but 61 -> 54 and 64 -> 57 with 4 and 8 heads).  With 128-byte rows units of 32
+// take 0-15 % longer, and units of 64 lose everywhere.
 #ifndef PKV_INT8_WARPS
 #define PKV_INT8_WARPS 4
-#endif
-#ifndef PKV_INT8_UNIT_TOKENS
-#define PKV_INT8_UNIT_TOKENS 16
 #endif
 #ifndef PKV_INT8_STAGES
 #define PKV_INT8_STAGES 2
@@ -420,7 +423,8 @@ int decode_fp8_by_block(int block_size, int group, const pkv::DecodeParams& prm,
 template <typename T, int D, int B, int G>
 int launch_decode_int8(const pkv::DecodeParams& prm, const pkv::Int8Maps& tm, int grid, const Launch& ln) {
     constexpr int NW = PKV_INT8_WARPS;
-    constexpr int U = B < PKV_INT8_UNIT_TOKENS ? PKV_INT8_UNIT_TOKENS / B : 1;
+    constexpr int kUnit = D == 64 && (B >= 16 || G >= 4) ? 32 : 16;
+    constexpr int U = B < kUnit ? kUnit / B : 1;
     constexpr int NST = PKV_INT8_STAGES;
     using C = pkv::DecodeInt8Cfg<D, B, G, NST, NW, U>;
     static size_t configured[64] = {};
