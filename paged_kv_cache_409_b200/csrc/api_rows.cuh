@@ -135,32 +135,46 @@ int launch_read(const pkv::ReadRowsParams& p, cudaStream_t s) {
     return launch_read_as<TD, 16>(p, s);
 }
 
-// CTAs that share an item's key tiles (a cluster of 1, 2, 4 or 8).  Measured on
-// B200: a key tile takes a CTA about 2.4 us, its start and end 9 us alone and
-// 13 us with the cluster's merge, and an SM holds one CTA.  So a launch of few
-// items is cut (8 items of 16385 keys, head_dim 128: 293 us in one part, 51 in
-// eight), one that fills the SMs is not (256 items of up to 66 tiles: 175 us in
-// one part, 202 in two).  The lengths are not known here: max_tiles is the
-// table's reach.
-int prefill_parts(int64_t items, int64_t max_tiles) {
+// CTAs that share an item's key tiles: a cluster of 1 to 8.  Measured on B200: a
+// key tile takes a CTA about 2.4 us, its start and end 9 us alone and 13 us
+// with the cluster's merge, and an SM holds one CTA.  So a launch of few items
+// is cut (8 items of 16385 keys, head_dim 128: 293 us in one part, 51 in eight),
+// one that fills the SMs is not (256 items of up to 66 tiles: 167 us in one
+// part, 202 in two).  fit[k]: clusters of k CTAs that run at once; a GPC's SMs
+// limit it (15 of eight, 22 of six: 16 items of 16128 keys take 108 us in
+// eight parts, whose last cluster runs alone, and 68 in six).  The lengths are
+// not known here: max_tiles is the table's reach.
+int prefill_parts(int64_t items, int64_t max_tiles, const int (&fit)[9]) {
+    auto cost = [&](int parts) {
+        const double waves = (double)items / fit[parts];
+        return (waves > 4 ? waves : std::ceil(waves)) * ((parts == 1 ? 9.0 : 13.0) + 2.4 * ceil_div(max_tiles, parts));
+    };
     int best = 1;
-    double best_us = 0;
-    for (int parts = 1; parts <= 8; parts *= 2) {
-        const double waves = std::max(1.0, (double)(items * parts) / sm_count());
-        const double us = waves * ((parts == 1 ? 9.0 : 13.0) + 2.4 * ceil_div(max_tiles, parts));
-        if (parts == 1 || us < 0.9 * best_us) best = parts, best_us = us;
-    }
+    double best_us = 0.9 * cost(1);  // the model's margin
+    for (int parts = 2; parts <= 8; ++parts)
+        if (fit[parts] > 0 && cost(parts) < best_us) best = parts, best_us = cost(parts);
     return best;
 }
 
 template <typename T, int D, int G>
 int launch_prefill_int8(const pkv::PrefillInt8Params& prm, const CUtensorMap& tq, const CUtensorMap& tk,
-                        const CUtensorMap& tv, int items, int parts, cudaStream_t s) {
+                        const CUtensorMap& tv, int items, int live_items, int64_t max_tiles, cudaStream_t s) {
     using C = pkv::PrefillInt8Cfg<D, G>;
     auto kern = pkv::paged_prefill_int8_kernel<T, D, G>;
     int dev = 0;
     PKV_CUDA(cudaGetDevice(&dev));
-    static bool configured[64] = {};
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(pkv::kPrefillInt8Threads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    static std::atomic<bool> configured[64];
+    static int fit[64][9];  // clusters of k CTAs that a device runs at once
     if (!configured[dev & 63]) {
         // the softmax threads' share (192) comes out of what the block is
         // launched with: 512 threads x 128 registers, no fewer
@@ -168,20 +182,17 @@ int launch_prefill_int8(const pkv::PrefillInt8Params& prm, const CUtensorMap& tq
         PKV_CUDA(cudaFuncGetAttributes(&a, kern));
         if (a.numRegs < 128) return PKV_EUNSUPPORTED;
         PKV_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+        cfg.numAttrs = 1;
+        for (int k = 1; k <= 8; ++k) {
+            cfg.gridDim = dim3((unsigned)k);
+            attr[0].val.clusterDim.x = k;
+            PKV_CUDA(cudaOccupancyMaxActiveClusters(&fit[dev & 63][k], kern, &cfg));
+        }
         configured[dev & 63] = true;
     }
-    cudaLaunchConfig_t cfg = {};
+    const int parts = prefill_parts(live_items, max_tiles, fit[dev & 63]);
     cfg.gridDim = dim3((unsigned)(items * parts));
-    cfg.blockDim = dim3(pkv::kPrefillInt8Threads);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = parts;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
     cfg.numAttrs = 2;
     PKV_CUDA(cudaLaunchKernelEx(&cfg, kern, prm, tq, tk, tv));
     PKV_CUDA(cudaGetLastError());
@@ -190,12 +201,12 @@ int launch_prefill_int8(const pkv::PrefillInt8Params& prm, const CUtensorMap& tq
 
 template <typename T, int D>
 int prefill_int8_by_group(int group, const pkv::PrefillInt8Params& prm, const CUtensorMap& tq, const CUtensorMap& tk,
-                          const CUtensorMap& tv, int items, int parts, cudaStream_t s) {
+                          const CUtensorMap& tv, int items, int live_items, int64_t max_tiles, cudaStream_t s) {
     switch (group) {
-        case 1: return launch_prefill_int8<T, D, 1>(prm, tq, tk, tv, items, parts, s);
-        case 2: return launch_prefill_int8<T, D, 2>(prm, tq, tk, tv, items, parts, s);
-        case 4: return launch_prefill_int8<T, D, 4>(prm, tq, tk, tv, items, parts, s);
-        case 8: return launch_prefill_int8<T, D, 8>(prm, tq, tk, tv, items, parts, s);
+        case 1: return launch_prefill_int8<T, D, 1>(prm, tq, tk, tv, items, live_items, max_tiles, s);
+        case 2: return launch_prefill_int8<T, D, 2>(prm, tq, tk, tv, items, live_items, max_tiles, s);
+        case 4: return launch_prefill_int8<T, D, 4>(prm, tq, tk, tv, items, live_items, max_tiles, s);
+        case 8: return launch_prefill_int8<T, D, 8>(prm, tq, tk, tv, items, live_items, max_tiles, s);
         default: return PKV_EUNSUPPORTED;
     }
 }
@@ -469,9 +480,11 @@ int pkv_paged_attention_prefill_chunk_int8(void* out, const void* query, const v
     const int64_t tile_pairs = ceil_div(ceil_div(max_q_len, tile_tokens), 2);
     const int64_t items = (int64_t)num_chunks * tile_pairs * num_kv_heads;
     if (items > INT32_MAX / 8) return PKV_EUNSUPPORTED;
-    // at most a last, short pair per chunk beyond the rows' worth of pairs
-    const int64_t pairs = std::min(num_chunks * tile_pairs, num_chunks + total_q_tokens / (2 * tile_tokens));
-    const int parts = prefill_parts(pairs * num_kv_heads, ceil_div((int64_t)max_blocks_per_seq * block_size, 128));
+    // items that exist, about: a chunk's last pair of tiles is half full on average
+    const int64_t pairs = std::min(num_chunks * tile_pairs,
+                                   std::max<int64_t>(num_chunks, (num_chunks + 1) / 2 + total_q_tokens / (2 * tile_tokens)));
+    const int live_items = (int)(pairs * num_kv_heads);
+    const int64_t max_tiles = ceil_div((int64_t)max_blocks_per_seq * block_size, 128);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (checked_mode()) {
         std::vector<int32_t> qsl, lens;
@@ -516,10 +529,10 @@ int pkv_paged_attention_prefill_chunk_int8(void* out, const void* query, const v
     prm.total_q_tokens = (int)total_q_tokens;
     const bool bf16 = dtype == PKV_BF16;
     if (head_dim == 64)
-        return bf16 ? prefill_int8_by_group<__nv_bfloat16, 64>(group, prm, tq, tk, tv, (int)items, parts, s)
-                    : prefill_int8_by_group<__half, 64>(group, prm, tq, tk, tv, (int)items, parts, s);
-    return bf16 ? prefill_int8_by_group<__nv_bfloat16, 128>(group, prm, tq, tk, tv, (int)items, parts, s)
-                : prefill_int8_by_group<__half, 128>(group, prm, tq, tk, tv, (int)items, parts, s);
+        return bf16 ? prefill_int8_by_group<__nv_bfloat16, 64>(group, prm, tq, tk, tv, (int)items, live_items, max_tiles, s)
+                    : prefill_int8_by_group<__half, 64>(group, prm, tq, tk, tv, (int)items, live_items, max_tiles, s);
+    return bf16 ? prefill_int8_by_group<__nv_bfloat16, 128>(group, prm, tq, tk, tv, (int)items, live_items, max_tiles, s)
+                : prefill_int8_by_group<__half, 128>(group, prm, tq, tk, tv, (int)items, live_items, max_tiles, s);
 }
 
 }  // extern "C"

@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
             // elements to a row add the parts up.
             float* weights = reinterpret_cast<float*>(smem + C::W_OFF);  // [row][8]
             const uint32_t base = smem_u32(smem);
-            const int rows = 256 / parts, rr0 = rank * rows;
+            const int rr0 = rank * 256 / parts, rows = (rank + 1) * 256 / parts - rr0;
             if (tid < rows) {
                 float m[8], l[8], mx = -INFINITY, least = 0.f, sum = 0.f;
 #pragma unroll

@@ -88,6 +88,20 @@ def test_prefill_few_items(case):
     assert torch.equal(bad[: sum(ns)][~want], out[: sum(ns)][~want])
 
 
+@pytest.mark.parametrize("G,D", [(1, 64), (2, 128)])
+@pytest.mark.parametrize("Hkv", [12, 16, 24, 30, 40, 60])
+def test_prefill_clusters_of_every_size(Hkv, G, D):
+    """Head counts that give clusters of 8, 6, 5, 4, 3 and 2 CTAs: shares of the key tiles and of the merged rows that
+    do not divide evenly."""
+    lens, ns = [2531], [101]
+    kp, vp, bt = make_pools(lens, 16, Hkv, D, seed=Hkv)
+    q = torch.randn(sum(ns), Hkv * G, D, device="cuda").half()
+    out = run(q, kp, vp, bt, ns, lens, D ** -0.5)
+    assert pkv.get_device_error() == 0
+    verify(out, q, kp, vp, bt, ns, lens, D ** -0.5, f"{Hkv} heads")
+    assert torch.equal(out, run(q, kp, vp, bt, ns, lens, D ** -0.5))
+
+
 def test_prefill_few_items_bad_tables_and_wait_limit():
     ns, lens = [5, 2], [3000, 2500]
     kp, vp, bt = make_pools(lens, 16, 2, 128, seed=9)
