@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(NW * 32) paged_decode_kernel(const DecodeParam
     decode_finish<T, D, G, NW>(p, red_m, s, g, part, direct);
 }
 
-// ---- log-sum-exp merge of the partitions: one warp per (sequence, q head).
+// ---- log-sum-exp merge of the partitions: W warps per (sequence, q head), 1 or 4.
 struct MergeParams {
     void* out;
     const int32_t* context_lens;
@@ -363,9 +363,10 @@ struct MergeParams {
     int num_partitions;
 };
 
-template <typename T, int D>
+template <typename T, int D, int W>
 __global__ void __launch_bounds__(128) paged_decode_merge_kernel(const MergeParams p) {
-    const int wid = blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int sub = W == 1 ? 0 : threadIdx.x >> 5;  // this warp's share of a row's parts
+    const int wid = W == 1 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
     const int lane = threadIdx.x & 31;
     if (wid >= p.num_seqs * p.num_q_heads) return;
     const int s = wid / p.num_q_heads;
@@ -391,17 +392,39 @@ __global__ void __launch_bounds__(128) paged_decode_merge_kernel(const MergePara
     float o[DPL];
 #pragma unroll
     for (int j = 0; j < DPL; ++j) o[j] = 0.f;
-    for (int i = 0; i < nparts; ++i) {
-        const float w = pm[i] == -INFINITY ? 0.f : pl[i] * exp2f(pm[i] - mx);
-        const float* src = po + static_cast<int64_t>(i) * D + lane * DPL;
-        if constexpr (DPL == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(src);
-            o[0] = fmaf(w, v.x, o[0]), o[1] = fmaf(w, v.y, o[1]), o[2] = fmaf(w, v.z, o[2]),
-            o[3] = fmaf(w, v.w, o[3]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < DPL; ++j) o[j] = fmaf(w, src[j], o[j]);
+    // The warps take runs of parts in turn; a lane has one part's weight, and the
+    // parts' rows are loaded eight at a time (one after the other a part costs
+    // 0.3 us: 19 us for the 74 parts of one sequence of 32768 tokens) and added
+    // in order.
+    constexpr int kRun = W == 1 ? 32 : 8;
+    for (int i0 = sub * kRun; i0 < nparts; i0 += W * kRun) {
+        const int i = i0 + lane;
+        const int n = min(kRun, nparts - i0);
+        const float wl = lane >= n || pm[i] == -INFINITY ? 0.f : pl[i] * exp2f(pm[i] - mx);
+        const float* src = po + static_cast<int64_t>(i0) * D + lane * DPL;
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+            const float w = __shfl_sync(0xffffffffu, wl, k);
+            if constexpr (DPL == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(src + k * D);
+                o[0] = fmaf(w, v.x, o[0]), o[1] = fmaf(w, v.y, o[1]), o[2] = fmaf(w, v.z, o[2]),
+                o[3] = fmaf(w, v.w, o[3]);
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(src + k * D);
+                o[0] = fmaf(w, v.x, o[0]), o[1] = fmaf(w, v.y, o[1]);
+            }
         }
+    }
+    if constexpr (W > 1) {  // the warps' sums, added in the order of the warps
+        __shared__ float red[W][D];
+#pragma unroll
+        for (int j = 0; j < DPL; ++j) red[sub][lane * DPL + j] = o[j];
+        __syncthreads();
+        if (sub > 0) return;
+#pragma unroll
+        for (int k = 1; k < W; ++k)
+#pragma unroll
+            for (int j = 0; j < DPL; ++j) o[j] += red[k][lane * DPL + j];
     }
     const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
     T* dst = reinterpret_cast<T*>(p.out) + static_cast<int64_t>(wid) * D + lane * DPL;
