@@ -163,8 +163,16 @@ __device__ __forceinline__ int sequence_by_length(const int32_t* lens, int n, in
     return found;
 }
 
+// CTAs per SM that the registers are told to allow.  Four (106-124 registers,
+// where the compiler by itself takes 96-98 at head dim 128 and 64-95 at 64) gain
+// up to 5 % where an MMA's columns are in use (256 sequences, 8 query heads each
+// of 128: 128 against 130 us; 4 heads, 128 sequences over [512, 4096]: 99 against
+// 104) and lose as much elsewhere (64 sequences x 32 heads of 128: 99 against 94
+// us; 8 query heads of 64: 62 against 58).
+constexpr int int8_min_ctas(int D, int G) { return (D == 128 ? G >= 4 : G < 8) ? 4 : 0; }
+
 template <typename T, int D, int B, int G, int NST, int NW, int U>
-__global__ void __launch_bounds__(NW * 32) paged_decode_int8_kernel(const DecodeParams p,
+__global__ void __launch_bounds__(NW * 32, int8_min_ctas(D, G)) paged_decode_int8_kernel(const DecodeParams p,
                                                                     const __grid_constant__ Int8Maps tm) {
     using C = DecodeInt8Cfg<D, B, G, NST, NW, U>;
     constexpr int kThreads = NW * 32;
