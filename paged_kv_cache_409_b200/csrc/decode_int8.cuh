@@ -31,8 +31,8 @@
 // same barrier.
 //
 // Bound by memory.  64 sequences of [128, 2048] tokens x 32 heads of 128, fp16:
-// 94 us, 6.35 TB/s (0.97 of a copy).  256 sequences x 8 KV heads, 8 query heads
-// each: 118-124 us, 5.9-6.2 TB/s; there the eight columns of an MMA are all in
+// 92-94 us, 6.4 TB/s (0.98 of a copy).  256 sequences x 8 KV heads, 8 query heads
+// each: 118-128 us, 5.7-6.2 TB/s; there the eight columns of an MMA are all in
 // use, and what is left is the ranking and the last wave.  Four warps of two
 // stages and units of 16 tokens: 8 warps, 2 warps, 3 stages and units of 32 are
 // all slower on the latter (172, 148, 145, 140 us when this version took 130).
