@@ -6,14 +6,25 @@
 //
 // Widening.  Tile rows arrive as codes (16 KB at head_dim 128) with one fp32
 // scale each.  A converter thread turns four codes into two f16 pairs: a byte
-// permute puts 0x64 over each code (1024 + u), a subtraction of 1152 leaves
-// u - 128 exactly, and scale * (u - 128) is formed as c * s_hi + c * s_lo with
-// the scale split in two f16 parts, so that what is rounded is the product
-// (2^-11 of the element; 2^-25 absolute below 2^-14), not the scale.  Rows past
-// the sequence and rows of bad blocks are written as zeros: P is zero there,
-// and 0 * NaN must not reach O.  For the same reason a V row whose scale is NaN
-// (or beyond f16) becomes zeros and its K row NaN: the scores that see the row
-// are NaN, those that the causal mask hides stay out of it.
+// permute puts 0x48 over each code (8 + u / 128), a subtraction of 9 leaves
+// c = (u - 128) / 128 exactly, and the element is c * hi + c * lo with S, 128
+// times the scale in the units below, split in two f16 parts (2^-22 of it), so that
+// what is rounded is the product: 2^-11 of the element.
+// Units.  f16 keeps those 11 bits over 30 binades only, and rows may be of any
+// size: rows of 1e-4 taken as they are came out 4 % off (the split itself fell
+// on the subnormal grid), rows of 3e-6 as zeros.  So the loader, which has a
+// tile's 128 scales in a warp's registers, gives every K tile a power of two of
+// its own that puts the largest S at 2^14 or above (never 2^15), and V a running
+// one, 2^12 or above for the largest row so far, which only grows: the scores
+// are multiplied back with the scale they take anyway, and O is rescaled, as for
+// a new maximum, in the few tiles where V's unit grows.  An f16 subnormal is then
+// below 2^-35 of the largest such row.  bf16 query rows are narrowed in units of
+// their own likewise.  All of it costs the softmax one 16-byte read and two
+// multiplications a tile.
+// Rows past the sequence and rows of bad blocks are written as zeros: P is zero
+// there, and 0 * NaN must not reach O.  For the same reason a V row whose scale is
+// NaN (or beyond f16's largest value / 127) becomes zeros and its K row NaN: the
+// scores that see the row are NaN, those that the causal mask hides stay out of it.
 //
 // Roles (512 threads; the registers of the second half go to the softmax):
 //   warps 0-7   softmax, four per query tile, as in prefill.cuh; with bf16
@@ -76,8 +87,9 @@ struct PrefillInt8Cfg {
     static constexpr int KC_OFF = V_OFF + 2 * KT_BYTES;  // staging of K, then of V
     static constexpr int VC_OFF = KC_OFF + C_BYTES;
     static constexpr int SC_OFF = VC_OFF + C_BYTES;      // scales: K [BN], V [2][BN] (tile j in j & 1)
-    static constexpr int BAR_OFF = SC_OFF + 3 * BN * 4;
-    static constexpr int NBAR = 26;
+    static constexpr int UNIT_OFF = SC_OFF + 3 * BN * 4;  // [4] units of tile j in j & 3
+    static constexpr int BAR_OFF = UNIT_OFF + 4 * 16;
+    static constexpr int NBAR = 28;
     static constexpr int SMEM = 1024 + BAR_OFF + NBAR * 8;
     static constexpr uint32_t TMEM_COLS = 512, S_COL0 = 0, O_COL0 = 256;
     static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -136,10 +148,23 @@ __device__ __forceinline__ uint32_t hfma2_u(uint32_t a, uint32_t b, uint32_t c) 
     return y;
 }
 
-// Four codes (one 32-bit word) times a scale split in two f16 parts.
+__device__ __forceinline__ uint32_t hsub2_9(uint32_t x) {
+    uint32_t y;
+    asm("add.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0xC880C880u));
+    return y;
+}
+
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+// The binade of a positive finite float's bits, no less than -100 (zeros, and
+// what would take a unit's inverse out of fp32).
+__device__ __forceinline__ int binade(uint32_t bits) { return max(static_cast<int>(bits >> 23) - 127, -100); }
+
+// Four codes (one 32-bit word), as (u - 128) / 128, times a number split in two f16 parts.
 __device__ __forceinline__ uint2 widen_codes4(uint32_t u, uint32_t s_hi, uint32_t s_lo) {
-    const uint32_t a = hsub2_1152(__byte_perm(u, 0x64646464u, 0x4140));
-    const uint32_t b = hsub2_1152(__byte_perm(u, 0x64646464u, 0x4342));
+    const uint32_t a = hsub2_9(__byte_perm(u, 0x48484848u, 0x4140));
+    const uint32_t b = hsub2_9(__byte_perm(u, 0x48484848u, 0x4342));
     return make_uint2(hfma2_u(a, s_hi, hmul2_u(a, s_lo)), hfma2_u(b, s_hi, hmul2_u(b, s_lo)));
 }
 
@@ -169,6 +194,7 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
     uint64_t* mma_done = bars + 20;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 22);
+    uint64_t* u_full = bars + 23;   // [4] units of tile j written, in j & 3
 
     griddep_wait();  // launched as a dependent of whatever comes before it
     const int parts = cluster_size(), rank = cluster_rank();
@@ -226,6 +252,7 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
             mbar_init(&p_full[i], 128);
             mbar_init(&o_full[i], 1);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(&u_full[i], 1);
         mbar_init(mma_done, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -263,6 +290,39 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
             // tile ahead of their use (copies of 32 to 128 bytes each would cost as
             // many bulk copies as the codes); rows of blocks that are not loaded
             // get 0: zeros.
+            // The largest scale a row may have: fp16's largest value / 127, and what
+            // the rounding of a scale adds.
+            constexpr float kMaxScale = 65504.f / 127.f * (1.f + 0x1p-20f);
+            int v_unit = -103;  // below every binade: the first tile sets it
+            // The fetched scales of tile j in its units, on their way to the
+            // converters (rows past the sequence 0; rows that do not fit: K NaN, V
+            // 0), and the units for the softmax: (K's, V's, V's last over V's, -).
+            auto scale_units = [&](int j, float4& ks4, float4& vs4) -> float4 {
+                float ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, vs[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
+                const int live = L - ((tb + j) * C::BN + 4 * lane);
+                uint32_t k_top = 0, v_top = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (i >= live) {
+                        ks[i] = vs[i] = 0.f;
+                    } else if (!(fabsf(ks[i]) <= kMaxScale && fabsf(vs[i]) <= kMaxScale)) {
+                        ks[i] = __uint_as_float(0x7fc00000u), vs[i] = 0.f;
+                    } else {
+                        k_top = max(k_top, abs_bits(ks[i])), v_top = max(v_top, abs_bits(vs[i]));
+                    }
+                }
+                const int k_unit = binade(__reduce_max_sync(0xffffffffu, k_top));
+                const int v_new = binade(__reduce_max_sync(0xffffffffu, v_top));
+                float grown = 1.f;
+                if (v_new > v_unit + 2) {  // S would pass 2^15
+                    grown = pow2(v_unit - v_new);
+                    v_unit = v_new;
+                }
+                const float km = pow2(14 - k_unit), vm = pow2(12 - v_unit);
+                ks4 = make_float4(ks[0] * km, ks[1] * km, ks[2] * km, ks[3] * km);
+                vs4 = make_float4(vs[0] * vm, vs[1] * vm, vs[2] * vm, vs[3] * vm);
+                return make_float4(pow2(k_unit - 7), pow2(v_unit - 5), grown, 0.f);
+            };
             auto fetch_scales = [&](int id, float4& ks, float4& vs) {
                 const int own = __shfl_sync(0xffffffffu, id, 4 * lane / B);
                 ks = vs = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -299,9 +359,17 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
             int loaded_k = 0, loaded_v = 0;
             for (int j = 0; j < nkt; ++j) {
                 const int ids_later = fetch_ids(j + 2);
+                const float4 units = scale_units(j, ks, vs);
                 if (j > 0 && !__all_sync(0xffffffffu, mbar_wait_or_abort_idle(&c_free[0], (j - 1) & 1, abort_flag))) break;
                 *reinterpret_cast<float4*>(scales + 4 * lane) = ks;
                 *reinterpret_cast<float4*>(scales + (1 + (j & 1)) * C::BN + 4 * lane) = vs;
+                // Read by the softmax threads of tile j, which are done with it before
+                // S(j + 1) runs, whose K stage tile j + 3 is widened into: j + 4 may
+                // overwrite it.
+                if (leader) {
+                    *reinterpret_cast<float4*>(smem + C::UNIT_OFF + (j & 3) * 16) = units;
+                    mbar_arrive(&u_full[j & 3]);
+                }
                 __syncwarp();
                 load_codes(0, &tm_k, ids);
                 loaded_k = j + 1;
@@ -396,19 +464,10 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
             // tile is D / 64 panels of 128-byte rows, swizzled over 128 bytes:
             // eight neighbouring lanes touch eight different 16-byte columns
             // of either.
-            constexpr float kMaxScale = 65504.f / 128.f;
             const int row = ct, sw = row & 7;
-            const float* vs_of = scales + C::BN + row;  // + (j & 1) * BN
             auto widen = [&](int which, int j, uint8_t* dst) {
                 const uint8_t* src = smem + (which ? C::VC_OFF : C::KC_OFF);
-                float s = vs_of[(j & 1) * C::BN];
-                if (which) {
-                    if (!(s <= kMaxScale)) s = 0.f;
-                } else {
-                    const float ks = scales[row];
-                    s = s <= kMaxScale && ks <= kMaxScale ? ks : __uint_as_float(0x7fc00000u);
-                }
-                if ((tb + j) * C::BN + row >= L) s = 0.f;
+                const float s = scales[(which ? 1 + (j & 1) : 0) * C::BN + row];
                 const __half hi = __float2half_rn(s);
                 const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(__float2half_rn(s - __half2float(hi)));
                 const uint32_t sh = *reinterpret_cast<const uint32_t*>(&hi2);
@@ -460,7 +519,7 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
         const int nk = x == 0 ? nka : nkb;
         const uint32_t ts = tmem + lane_base + C::S_COL0 + 128 * x;
         const uint32_t to = tmem + lane_base + C::O_COL0 + D * x;
-        const float sl2 = p.scale_log2;
+        float q_unit = 1.f, v_unit = 1.f;  // of this thread's query row; of O
         constexpr float kRescaleLog2 = 8.f;
         float m_used = -INFINITY, lsum = 0.f;
         bool ok = true;
@@ -468,16 +527,32 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
             ok = nkt > 0 && __all_sync(0xffffffffu, mbar_wait_or_abort(q_full, 0, abort_flag));
             if (ok) {
                 if (x == 0 || has_b) {
-                    uint8_t* q = smem + C::Q_OFF + x * C::Q_BYTES;
+                    // A row per thread: its largest element, then every element in
+                    // the row's unit (16-byte columns in the order of the swizzle:
+                    // eight lanes touch eight different ones).
+                    uint8_t* q = smem + C::Q_OFF + x * C::Q_BYTES + row * 128;
+                    uint32_t top2 = 0;
 #pragma unroll 4
-                    for (int off = row * 16; off < C::Q_BYTES; off += 128 * 16) {
-                        uint4 v = *reinterpret_cast<const uint4*>(q + off);
-                        auto narrow = [](uint32_t u) {
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(q + (c >> 3) * C::BM * 128 + (((c ^ row) & 7) << 4));
+                        top2 = __vmaxu2(__vmaxu2(top2, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
+                                        __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+                    }
+                    const uint32_t top = max(top2 & 0xffffu, top2 >> 16) << 16;
+                    float mul = 1.f;
+                    if (top < 0x7f800000u) {  // else NaN or an infinity, which shows in the result
+                        q_unit = pow2(binade(top) - 14);
+                        mul = pow2(14 - binade(top));
+                    }
+#pragma unroll 4
+                    for (int c = 0; c < D / 8; ++c) {
+                        uint4* at = reinterpret_cast<uint4*>(q + (c >> 3) * C::BM * 128 + (((c ^ row) & 7) << 4));
+                        const uint4 v = *at;
+                        auto narrow = [&](uint32_t u) {
                             const float2 f = Elem<__nv_bfloat16>::pair(u);
-                            return pack_half2(f.x, f.y);
+                            return pack_half2(f.x * mul, f.y * mul);
                         };
-                        v = make_uint4(narrow(v.x), narrow(v.y), narrow(v.z), narrow(v.w));
-                        *reinterpret_cast<uint4*>(q + off) = v;
+                        *at = make_uint4(narrow(v.x), narrow(v.y), narrow(v.z), narrow(v.w));
                     }
                     fence_proxy_async();
                 }
@@ -485,11 +560,15 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
             }
         }
         for (int j = 0; ok && j < nk; ++j) {
-            if (!__all_sync(0xffffffffu, mbar_wait_or_abort(&s_full[x], j & 1, abort_flag))) {
+            if (!__all_sync(0xffffffffu, mbar_wait_or_abort(&u_full[j & 3], (j >> 2) & 1, abort_flag) &&
+                                             mbar_wait_or_abort(&s_full[x], j & 1, abort_flag))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
+            const float4 units = *reinterpret_cast<const float4*>(smem + C::UNIT_OFF + (j & 3) * 16);
+            const float sl2 = p.scale_log2 * (q_unit * units.x);
+            v_unit = units.y;
             float sv[C::BN];
             {
                 uint32_t u[C::BN];
@@ -554,7 +633,8 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
                 tmem_st16_nowait(ts + c * 16, pw);
             }
             lsum = lsum * alpha + ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y));
-            if (j >= 1 && __any_sync(0xffffffffu, rescale && alpha != 1.f)) {
+            alpha *= units.z;
+            if (j >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     float v[32];
@@ -574,7 +654,7 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
         if (parts == 1) {
             if (have) {
                 const bool live = tok < n && !*abort_flag;
-                const float inv = 1.f / lsum;
+                const float inv = v_unit / lsum;
                 T* dst = out + (static_cast<int64_t>(q0 + tok) * p.num_q_heads + static_cast<int64_t>(g) * G + row % G) * D;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
@@ -607,7 +687,7 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
 #pragma unroll
                     for (int d = 0; d < 8; ++d)
                         *reinterpret_cast<float4*>(smem + r256 * D * 4 + (((c * 8 + d) ^ (row & 7)) << 4)) =
-                            make_float4(v[4 * d], v[4 * d + 1], v[4 * d + 2], v[4 * d + 3]);
+                            make_float4(v[4 * d] * v_unit, v[4 * d + 1] * v_unit, v[4 * d + 2] * v_unit, v[4 * d + 3] * v_unit);
                 }
             }
             *reinterpret_cast<float2*>(smem + C::ML_OFF + r256 * 8) =
