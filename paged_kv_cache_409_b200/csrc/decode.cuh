@@ -373,8 +373,11 @@ __global__ void __launch_bounds__(128) paged_decode_merge_kernel(const MergePara
     const int nblk = decode_seq_blocks(p.context_lens[s], p.block_size, p.max_blocks_per_seq,
                                        p.num_partitions * p.partition_blocks, false);
     const int nparts = nblk > 0 ? (nblk + p.partition_blocks - 1) / p.partition_blocks : 1;
+    // The partials are the writes of the decode grid.  Rows without any wait too:
+    // a dependent launch behind this grid waits for this grid alone, which must
+    // not complete before the decode has.
+    griddep_wait();
     if (nparts <= 1) return;  // the decode kernel wrote this row itself
-    griddep_wait();           // the partials are the writes of the decode grid
     const float* pm = p.ws_max + static_cast<int64_t>(wid) * p.num_partitions;
     const float* pl = p.ws_sum + static_cast<int64_t>(wid) * p.num_partitions;
     const float* po = p.ws_out + static_cast<int64_t>(wid) * p.num_partitions * D;

@@ -957,7 +957,7 @@ __global__ void __launch_bounds__(128) paged_decode_multi_merge_kernel(const Mul
     const int64_t row = wid / p.num_q_heads;
     // the chunk that owns this row: the last r with query_start_loc[r] <= row
     int lo = 0, hi = p.num_chunks;  // invariant: qsl[lo] <= row < qsl[hi] (when row is covered)
-    if (row < p.query_start_loc[0] || row >= p.query_start_loc[p.num_chunks]) return;
+    const bool covered = row >= p.query_start_loc[0] && row < p.query_start_loc[p.num_chunks];
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (p.query_start_loc[mid] <= row) lo = mid; else hi = mid;
@@ -965,8 +965,11 @@ __global__ void __launch_bounds__(128) paged_decode_multi_merge_kernel(const Mul
     const int nblk = decode_seq_blocks(p.seq_lens[lo], p.block_size, p.max_blocks_per_seq,
                                        p.num_partitions * p.partition_blocks, false);
     const int nparts = nblk > 0 ? (nblk + p.partition_blocks - 1) / p.partition_blocks : 1;
-    if (nparts <= 1) return;  // the attention kernel wrote this row itself
-    griddep_wait();           // the partials are the writes of the attention grid
+    // The partials are the writes of the attention grid.  Every row waits: a
+    // dependent launch behind this grid waits for this grid alone, which must not
+    // complete before the attention has.
+    griddep_wait();
+    if (!covered || nparts <= 1) return;  // no chunk's row, or written by the attention kernel itself
     const float* pm = p.ws_max + wid * p.num_partitions;
     const float* pl = p.ws_sum + wid * p.num_partitions;
     const float* po = p.ws_out + wid * p.num_partitions * D;

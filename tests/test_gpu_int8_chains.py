@@ -1,0 +1,59 @@
+"""Calls whose kernels are dependent launches, one behind the other without a synchronisation: each sees what those before it
+wrote, also behind a merge that has no row to merge."""
+import pytest
+import torch
+
+import paged_kv_cache_409_b200 as pkv
+from int8_helpers import make_pools
+
+pytestmark = pytest.mark.gpu
+
+
+def chained(attend, T, H, D, rounds=20):
+    """`attend(q, out)` then the append of its result and its read back, over and over; the reads with and without a
+    synchronisation behind every call."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    qs = [torch.randn(T, H, D, device="cuda", generator=g).half() for _ in range(rounds)]
+    pool = [torch.zeros(-(-T // 16) + 1, 16, H, D + 4, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    slots = torch.randperm(T, device="cuda", generator=g)
+    results = []
+    for sync in (True, False):
+        out, reads = torch.empty_like(qs[0]), [torch.empty(2, T, H, D, device="cuda") for _ in range(rounds)]
+        torch.cuda.synchronize()
+        for q, r in zip(qs, reads):
+            for call in (lambda: attend(q, out), lambda: pkv.reshape_and_cache_int8(out, out, *pool, slots),
+                         lambda: pkv.read_cache_int8(r[0], r[1], *pool, slots)):
+                call()
+                if sync:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        results.append(reads)
+    assert pkv.get_device_error() == 0
+    for a, b in zip(*results):
+        assert torch.equal(a, b) and bool(a.abs().sum() > 0)
+
+
+@pytest.mark.parametrize("kind", ["f16", "int8"])
+@pytest.mark.parametrize("lens", [[16] * 300, [16, 1, 700, 15] * 20], ids=["one part each", "some in parts"])
+def test_append_behind_a_decode_and_its_merge(kind, lens):
+    S, Hq, Hkv, D, B = len(lens), 8, 2, 64, 16
+    kp, vp, bt = make_pools(lens, B, Hkv, D, seed=1)
+    bt = torch.cat([bt, bt.new_full((S, 60), -1)], 1).contiguous()
+    cl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    if kind == "f16":
+        kp, vp = (torch.randn(kp.shape[0], B, Hkv, D, device="cuda").half() for _ in range(2))
+    call = pkv.paged_attention_decode if kind == "f16" else pkv.paged_attention_decode_int8
+    ws = torch.empty(pkv.decode_workspace_size(S, Hq, D, 1000, 16), dtype=torch.uint8, device="cuda")
+    chained(lambda q, out: call(out, q, kp, vp, bt, cl, 0.1, 1000, partition_size=16, workspace=ws), S, Hq, D)
+
+
+def test_append_behind_a_multi_token_call_and_its_merge():
+    R, n, Hq, Hkv, D, B = 40, 3, 8, 2, 64, 16
+    lens = torch.full((R,), 30, dtype=torch.int32, device="cuda")
+    NB = R * 2
+    kp, vp = (torch.randn(NB, B, Hkv, D, device="cuda").half() for _ in range(2))
+    bt = torch.full((R, 64), -1, dtype=torch.int32, device="cuda")
+    bt[:, :2] = torch.randperm(NB, device="cuda").view(R, 2).to(torch.int32)
+    qsl = torch.arange(0, R * n + 1, n, dtype=torch.int32, device="cuda")
+    chained(lambda q, out: pkv.paged_attention_decode_multi(out, q, kp, vp, bt, lens, qsl, n, 1000, 0.1, partition_size=64), R * n,
+            Hq, D)
