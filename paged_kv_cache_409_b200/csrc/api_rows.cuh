@@ -174,21 +174,25 @@ int launch_prefill_int8(const pkv::PrefillInt8Params& prm, const CUtensorMap& tq
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     static std::atomic<bool> configured[64];
-    static int fit[64][9];  // clusters of k CTAs that a device runs at once
+    static std::mutex filling;
+    static int fit[64][9];  // clusters of k CTAs that a device runs at once; written once, under the lock
     if (!configured[dev & 63]) {
-        // the softmax threads' share (192) comes out of what the block is
-        // launched with: 512 threads x 128 registers, no fewer
-        cudaFuncAttributes a;
-        PKV_CUDA(cudaFuncGetAttributes(&a, kern));
-        if (a.numRegs < 128) return PKV_EUNSUPPORTED;
-        PKV_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
-        cfg.numAttrs = 1;
-        for (int k = 1; k <= 8; ++k) {
-            cfg.gridDim = dim3((unsigned)k);
-            attr[0].val.clusterDim.x = k;
-            PKV_CUDA(cudaOccupancyMaxActiveClusters(&fit[dev & 63][k], kern, &cfg));
+        std::lock_guard<std::mutex> lock(filling);
+        if (!configured[dev & 63]) {
+            // the softmax threads' share (192) comes out of what the block is
+            // launched with: 512 threads x 128 registers, no fewer
+            cudaFuncAttributes a;
+            PKV_CUDA(cudaFuncGetAttributes(&a, kern));
+            if (a.numRegs < 128) return PKV_EUNSUPPORTED;
+            PKV_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+            cfg.numAttrs = 1;
+            for (int k = 1; k <= 8; ++k) {
+                cfg.gridDim = dim3((unsigned)k);
+                attr[0].val.clusterDim.x = k;
+                PKV_CUDA(cudaOccupancyMaxActiveClusters(&fit[dev & 63][k], kern, &cfg));
+            }
+            configured[dev & 63] = true;
         }
-        configured[dev & 63] = true;
     }
     const int parts = prefill_parts(live_items, max_tiles, fit[dev & 63]);
     cfg.gridDim = dim3((unsigned)(items * parts));

@@ -285,15 +285,26 @@ constexpr int pick_stages(int stage_bytes, int warps) {
     return n;
 }
 
+// The largest dynamic shared memory size set so far for a kernel, per device.
+// It only grows, under the lock: a thread that set a smaller size after another's
+// larger one would have that one's launch refused.
+struct SmemLimit {
+    std::atomic<size_t> have[64] = {};
+    std::mutex growing;
+};
+
 template <typename Kern, typename... Maps>
-int launch_decode_kernel(Kern kern, size_t smem, int threads, int grid, const Launch& ln, size_t* configured,
+int launch_decode_kernel(Kern kern, size_t smem, int threads, int grid, const Launch& ln, SmemLimit& limit,
                          const pkv::DecodeParams& prm, const Maps&... maps) {
     int dev = 0;
     PKV_CUDA(cudaGetDevice(&dev));
-    size_t& have = configured[dev & 63];  // largest dynamic smem size set so far on this device
+    std::atomic<size_t>& have = limit.have[dev & 63];
     if (smem > have) {
-        PKV_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-        have = smem;
+        std::lock_guard<std::mutex> lock(limit.growing);
+        if (smem > have) {
+            PKV_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+            have = smem;
+        }
     }
     return launch_kernel(kern, dim3(grid), dim3(threads), smem, ln, prm, maps...);
 }
@@ -310,7 +321,7 @@ int launch_decode(const pkv::DecodeParams& prm, const CUtensorMap& tk, const CUt
     constexpr int NST = pick_stages(STAGE, NW);
     using C = pkv::DecodeCfg<T, D, B, G, NST, NW>;
     const size_t smem = C::smem_bytes(prm.partition_blocks);
-    static size_t configured[64] = {};
+    static SmemLimit configured;
     // 16-bit types run the Q.K / P.V products on warp MMAs (one head per KV
     // head included: measured 6.6 vs 6.2 TB/s on the llama7b batch); fp32
     // stays on the CUDA cores.
@@ -379,7 +390,7 @@ int launch_decode_fp8(const pkv::DecodeParams& prm, const CUtensorMap& tk, const
     constexpr int NW = PKV_FP8_WARPS;
     constexpr int NST = std::max(1, std::min(8, (U > 1 ? 2 : 1) * PKV_FP8_STAGE_BUDGET / (NW * STAGE)));
     using C = pkv::DecodeFp8Cfg<B, G, NST, NW, U>;
-    static size_t configured[64] = {};
+    static SmemLimit configured;
     return launch_decode_kernel(pkv::paged_decode_fp8_kernel<T, B, G, NST, NW, U>, C::smem_bytes(prm.partition_blocks),
                                 NW * 32, grid, ln, configured, prm, tk, tv);
 }
@@ -428,7 +439,7 @@ int launch_decode_int8(const pkv::DecodeParams& prm, const pkv::Int8Maps& tm, in
     constexpr int U = B < kUnit ? kUnit / B : 1;
     constexpr int NST = PKV_INT8_STAGES;
     using C = pkv::DecodeInt8Cfg<D, B, G, NST, NW, U>;
-    static size_t configured[64] = {};
+    static SmemLimit configured;
     return launch_decode_kernel(pkv::paged_decode_int8_kernel<T, D, B, G, NST, NW, U>,
                                 C::smem_bytes(prm.partition_blocks), NW * 32, grid, ln, configured, prm, tm);
 }
@@ -466,8 +477,8 @@ int launch_multi(const pkv::MultiParams& prm, int lpt, const CUtensorMap& tq, co
     auto kern = pkv::paged_decode_multi_kernel<T, D>;
     int dev = 0;
     PKV_CUDA(cudaGetDevice(&dev));
-    static int resident[64] = {};  // CTAs per SM, per device (0: not configured yet)
-    int& per_sm = resident[dev & 63];
+    static std::atomic<int> resident[64];  // CTAs per SM, per device (0: not configured yet)
+    std::atomic<int>& per_sm = resident[dev & 63];
     if (per_sm == 0) {
         PKV_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
         int n = 0;
@@ -517,7 +528,7 @@ int launch_prefill(const pkv::PrefillParams& prm, const CUtensorMap& tq, const C
     auto kern = pkv::paged_prefill_kernel<T, D, G, TO>;
     int dev = 0;
     PKV_CUDA(cudaGetDevice(&dev));
-    static bool configured[64] = {};
+    static std::atomic<bool> configured[64];
     if (!configured[dev & 63]) {
         PKV_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
         configured[dev & 63] = true;
