@@ -229,7 +229,7 @@ int pkv_rope_and_cache_int8(void* query_out, const void* query, const void* key,
                             pkv_stream_t stream);
 
 /* Bytes of one block of an int8 pool: block_size * num_kv_heads * (head_dim +
- * 4); PKV_EINVAL for sizes <= 0. */
+ * 4); PKV_EINVAL for sizes <= 0 or a product beyond int64. */
 int64_t pkv_int8_block_bytes(int block_size, int num_kv_heads, int head_dim);
 
 /* Write new tokens' K and V rows into int8 pools, quantising on the way.

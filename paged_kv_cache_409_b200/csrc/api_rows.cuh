@@ -13,8 +13,11 @@ constexpr int kMaxRowHeads = 1 << 15;
 // The shape rules of int8 pools: 16-byte rows of codes and 16-byte blocks.
 bool int8_shape(int num_kv_heads, int head_dim, int block_size) {
     return head_dim % 16 == 0 && head_dim <= 256 && (int64_t)block_size * num_kv_heads % 4 == 0 &&
-           (int64_t)block_size * num_kv_heads * (head_dim + 4) <= INT32_MAX;
+           (int64_t)block_size * num_kv_heads <= INT32_MAX / (head_dim + 4);
 }
+
+// Slots of a pool are counted in 64 bits.
+bool countable_slots(int64_t num_blocks, int block_size) { return num_blocks <= INT64_MAX / block_size; }
 
 int check_slots(const int64_t* slot_mapping, int64_t num_tokens, int64_t num_slots, cudaStream_t s) {
     if (!checked_mode()) return PKV_OK;
@@ -32,7 +35,9 @@ int rows_int8_check(const void* x, const void* y, const void* key_cache, const v
                     const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads, int head_dim, int block_size,
                     int64_t num_blocks, int dtype) {
     if (!query_type(dtype)) return PKV_EUNSUPPORTED;
-    if (num_tokens < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0) return PKV_EINVAL;
+    if (num_tokens < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0 ||
+        !countable_slots(num_blocks, block_size))
+        return PKV_EINVAL;
     if (!int8_shape(num_kv_heads, head_dim, block_size)) return PKV_EUNSUPPORTED;
     if (num_tokens == 0) return PKV_OK;
     if (num_tokens > INT32_MAX || num_kv_heads > kMaxRowHeads) return PKV_EUNSUPPORTED;
@@ -224,7 +229,7 @@ int rope_impl(void* query_out, const void* query, const void* key, const void* v
               float v_scale, pkv_stream_t stream) {
     if (!query_type(dtype)) return PKV_EUNSUPPORTED;
     if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
-        num_blocks <= 0 || rotary_dim < 0 || rotary_dim > head_dim || max_position < 0 || !(eps >= 0.f) ||
+        num_blocks <= 0 || !countable_slots(num_blocks, block_size) || rotary_dim < 0 || rotary_dim > head_dim || max_position < 0 || !(eps >= 0.f) ||
         !std::isfinite(eps))
         return PKV_EINVAL;
     if (kPool == pkv::kPoolE4M3 &&
@@ -369,6 +374,7 @@ int pkv_rope_and_cache_int8(void* query_out, const void* query, const void* key,
 
 int64_t pkv_int8_block_bytes(int block_size, int num_kv_heads, int head_dim) {
     if (block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0) return PKV_EINVAL;
+    if ((int64_t)block_size * num_kv_heads > INT64_MAX / ((int64_t)head_dim + 4)) return PKV_EINVAL;
     return (int64_t)block_size * num_kv_heads * ((int64_t)head_dim + 4);
 }
 

@@ -1,0 +1,36 @@
+"""The row calls and calls over int8 pools without a GPU: sizes whose products leave their integers, tensors of another device,
+empty batches, and a step that checked mode refuses."""
+import pytest
+
+import paged_kv_cache_409_b200 as pkv
+
+EINVAL, EUNSUPPORTED = -1, -2
+P = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from paged_kv_cache_409_b200 import build
+    build.build()
+    return pkv.load_library()
+
+
+def test_block_bytes_beyond_64_bits_are_refused(lib):
+    big = 2**31 - 1
+    for sizes in ((2**30, 2**30, 2**30), (big, big, big), (big, big, 1), (2**30, 2**30, 4)):
+        b, h, d = sizes
+        assert lib.pkv_int8_block_bytes(b, h, d) == (b * h * (d + 4) if b * h * (d + 4) < 2**63 else EINVAL), sizes
+    assert lib.pkv_int8_block_bytes(2**30, 2, 2**30) == 2**31 * (2**30 + 4)
+
+
+def test_pools_of_uncountable_slots_are_refused(lib):
+    for fn in (lib.pkv_reshape_and_cache_int8, lib.pkv_read_cache_int8):
+        assert fn(P, P, P, P, P, 0, 2, 64, 16, 2**63 // 16 - 1, 1, None) == 0
+        assert fn(P, P, P, P, P, 0, 2, 64, 16, 2**63 // 16, 1, None) == EINVAL
+        assert fn(P, P, P, P, P, 0, 2**31 - 4, 64, 2**31 - 4, 4, 1, None) == EUNSUPPORTED
+
+    def rope(fn, blocks):
+        return fn(P, P, P, P, 512, 128, 128, 0, 0, 1e-6, P, 9, 64, 0, P, P, P, P, 0, 8, 2, 64, 16, blocks, 1, *tail, None)
+
+    for fn, tail in ((lib.pkv_rope_and_cache, ()), (lib.pkv_rope_and_cache_fp8, (1.0, 1.0)), (lib.pkv_rope_and_cache_int8, ())):
+        assert rope(fn, 2**63 // 16 - 1) == 0 and rope(fn, 2**63 // 16) == EINVAL
