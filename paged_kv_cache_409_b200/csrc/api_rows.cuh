@@ -452,6 +452,9 @@ int pkv_paged_attention_decode_step_int8(const void* new_keys, const void* new_v
     rc = rows_int8_check(new_keys, new_values, key_cache, value_cache, slot_mapping, num_new_tokens, num_kv_heads,
                          head_dim, block_size, num_blocks, dtype);
     if (rc) return rc;
+    rc = check_step_tables(block_tables, context_lens, num_seqs, max_blocks_per_seq, block_size, num_blocks,
+                           max_context_len, stream);
+    if (rc) return rc;
     rc = pkv_reshape_and_cache_int8(new_keys, new_values, key_cache, value_cache, slot_mapping, num_new_tokens,
                                     num_kv_heads, head_dim, block_size, num_blocks, dtype, stream);
     if (rc) return rc;

@@ -240,6 +240,14 @@ int check_tables(const int32_t* d_bt, const int32_t* d_lens, int num_seqs, int m
     return PKV_OK;
 }
 
+// A step's tables, before its append is launched.
+int check_step_tables(const int32_t* block_tables, const int32_t* context_lens, int num_seqs, int max_blocks_per_seq,
+                      int block_size, int64_t num_blocks, int max_context_len, pkv_stream_t stream) {
+    if (!checked_mode() || num_seqs == 0) return PKV_OK;
+    return check_tables(block_tables, context_lens, num_seqs, max_blocks_per_seq, block_size, num_blocks,
+                        max_context_len, static_cast<cudaStream_t>(stream));
+}
+
 // ------------------------------------------------------------ launches
 // Stream of a launch and whether the kernel may start as a programmatic
 // dependent of the kernel before it in the stream (its prologue overlapping
@@ -1036,6 +1044,9 @@ int pkv_paged_attention_decode_step(const void* new_keys, const void* new_values
     rc = reshape_check(new_keys, new_values, key_cache, value_cache, slot_mapping, num_new_tokens, num_kv_heads,
                        head_dim, block_size, num_blocks, dtype, false);
     if (rc) return rc;
+    rc = check_step_tables(block_tables, context_lens, num_seqs, max_blocks_per_seq, block_size, num_blocks,
+                           max_context_len, stream);
+    if (rc) return rc;
     rc = pkv_reshape_and_cache(new_keys, new_values, key_cache, value_cache, slot_mapping, num_new_tokens,
                                num_kv_heads, head_dim, block_size, num_blocks, dtype, stream);
     if (rc) return rc;
@@ -1062,6 +1073,9 @@ int pkv_paged_attention_decode_step_fp8(const void* new_keys, const void* new_va
     if (rc) return rc;
     rc = reshape_fp8_check(new_keys, new_values, key_cache, value_cache, slot_mapping, num_new_tokens, num_kv_heads,
                            head_dim, block_size, num_blocks, dtype);
+    if (rc) return rc;
+    rc = check_step_tables(block_tables, context_lens, num_seqs, max_blocks_per_seq, block_size, num_blocks,
+                           max_context_len, stream);
     if (rc) return rc;
     rc = pkv_reshape_and_cache_fp8(new_keys, new_values, key_cache, value_cache, slot_mapping, num_new_tokens,
                                    num_kv_heads, head_dim, block_size, num_blocks, dtype, k_scale, v_scale, stream);

@@ -57,3 +57,44 @@ def test_append_behind_a_multi_token_call_and_its_merge():
     qsl = torch.arange(0, R * n + 1, n, dtype=torch.int32, device="cuda")
     chained(lambda q, out: pkv.paged_attention_decode_multi(out, q, kp, vp, bt, lens, qsl, n, 1000, 0.1, partition_size=64), R * n,
             Hq, D)
+
+
+def test_a_step_that_checked_mode_refuses_has_changed_nothing():
+    """PKV_CHECK=1: a step with a bad table, or a bad length, writes no row of its new tokens."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import torch, paged_kv_cache_409_b200 as pkv
+i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device='cuda')
+B, H, D = 16, 2, 128
+bt = i32(0, 1, 2, 3).view(2, 2)
+bad = i32(0, 1, 2, 4).view(2, 2)
+slots = torch.tensor([3, 35], device='cuda')
+q = torch.randn(2, 4, D, device='cuda').half()
+k = torch.randn(2, H, D, device='cuda').half()
+pools = {'f16': lambda: torch.zeros(4, B, H, D, dtype=torch.half, device='cuda'),
+         'fp8': lambda: torch.zeros(4, B, H, D, dtype=torch.uint8, device='cuda'),
+         'int8': lambda: torch.zeros(4, B, H, D + 4, dtype=torch.uint8, device='cuda')}
+for kind, make in pools.items():
+    kp, vp = make(), make()
+    call = {'f16': pkv.paged_attention_decode_step, 'fp8': pkv.paged_attention_decode_step_fp8,
+            'int8': pkv.paged_attention_decode_step_int8}[kind]
+    scales = (0.1, 0.1) if kind == 'fp8' else ()
+    for tables, lens in ((bad, i32(20, 20)), (bt, i32(20, 33)), (bt, i32(-1, 20))):
+        try:
+            call(k, k, slots, torch.empty_like(q), q, kp, vp, tables, lens, 0.1, *scales, 32)
+            raise SystemExit(kind + ' was not refused')
+        except pkv.PagedKVError as e:
+            assert e.status == -3, e
+        torch.cuda.synchronize()
+        assert not kp.any() and not vp.any(), kind
+    call(k, k, slots, torch.empty_like(q), q, kp, vp, bt, i32(20, 20), 0.1, *scales, 32)
+    torch.cuda.synchronize()
+    assert kp.any() and vp.any()
+print('refused')
+"""
+    env = dict(os.environ, PKV_CHECK="1", PYTHONPATH=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=200)
+    assert r.returncode == 0 and "refused" in r.stdout, r.stdout + r.stderr
