@@ -12,6 +12,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <mutex>
 #include <set>
 #include <vector>
@@ -214,7 +215,12 @@ int sm_count() {
 // ------------------------------------------------------------ checked mode
 template <typename I>
 int fetch(std::vector<I>& host, const I* dev, size_t n, cudaStream_t s) {
-    host.resize(n);
+    try {
+        host.resize(n);
+    } catch (const std::exception&) {  // nothing may be thrown through a C entry
+        snprintf(g_last_cuda_error, sizeof g_last_cuda_error, "no host memory for a checked copy of %zu entries", n);
+        return PKV_ECUDA;
+    }
     if (n == 0) return PKV_OK;
     PKV_CUDA(cudaMemcpyAsync(host.data(), dev, n * sizeof(I), cudaMemcpyDeviceToHost, s));
     PKV_CUDA(cudaStreamSynchronize(s));

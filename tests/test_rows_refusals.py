@@ -34,3 +34,28 @@ def test_pools_of_uncountable_slots_are_refused(lib):
 
     for fn, tail in ((lib.pkv_rope_and_cache, ()), (lib.pkv_rope_and_cache_fp8, (1.0, 1.0)), (lib.pkv_rope_and_cache_int8, ())):
         assert rope(fn, 2**63 // 16 - 1) == 0 and rope(fn, 2**63 // 16) == EINVAL
+
+
+def test_checked_mode_without_host_memory_is_an_error():
+    """PKV_CHECK=1 copies the tables to the host: when there is no memory for that, the call fails, and the process goes on."""
+    import subprocess
+    import sys
+
+    from paged_kv_cache_409_b200 import build
+    code = f"""
+import ctypes, os, resource
+os.environ['PKV_CHECK'] = '1'
+lib = ctypes.CDLL({build.build()!r})
+resource.setrlimit(resource.RLIMIT_AS, (4 << 30, 4 << 30))
+I, L, V = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p
+P = V({P})
+n = L(2**31 - 1)  # 16 GiB of slots
+args = [P, P, P, P, P, n, I(2), I(64), I(16), L(4), I(1)]
+for name in ('pkv_reshape_and_cache_int8', 'pkv_read_cache_int8', 'pkv_reshape_and_cache'):
+    assert getattr(lib, name)(*args, V()) == -4, name
+lib.pkv_last_cuda_error.restype = ctypes.c_char_p
+assert b'memory' in lib.pkv_last_cuda_error()
+print('refused')
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=200)
+    assert r.returncode == 0 and "refused" in r.stdout, (r.returncode, r.stdout + r.stderr)
