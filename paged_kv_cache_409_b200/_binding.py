@@ -666,12 +666,14 @@ def rope_and_cache(query_out, query, key, value, cos_sin, positions, key_cache, 
 def rope_and_cache_fp8(query_out, query, key, value, cos_sin, positions, key_cache, value_cache, slot_mapping, k_scale,
                        v_scale, interleaved=False, q_norm_weight=None, k_norm_weight=None, eps=1e-6, stream=None):
     """:func:`rope_and_cache` into E4M3 pools."""
-    if key_cache.shape != value_cache.shape:
-        raise ValueError("the pools must have one shape")
+    shape = key_cache.shape
+    if value_cache.shape != shape or key_cache.dtype not in FP8_POOL_DTYPES or value_cache.dtype not in FP8_POOL_DTYPES:
+        raise ValueError("the pools must be uint8 or float8_e4m3fn pools of E4M3 codes, of one shape")
+    dev = _device(query, "query")
     return _rope_and_cache((_lib or load_library()).pkv_rope_and_cache_fp8, query_out, query, key, value, cos_sin,
-                           positions, _device(query, "query"), _fp8_pool(key_cache, "key_cache"),
-                           _fp8_pool(value_cache, "value_cache"), key_cache.shape, slot_mapping, interleaved,
-                           q_norm_weight, k_norm_weight, eps, (float(k_scale), float(v_scale)), stream)
+                           positions, dev, _at(key_cache, "key_cache", dev), _at(value_cache, "value_cache", dev), shape,
+                           slot_mapping, interleaved, q_norm_weight, k_norm_weight, eps, (float(k_scale), float(v_scale)),
+                           stream)
 
 
 def rope_and_cache_int8(query_out, query, key, value, cos_sin, positions, key_cache, value_cache, slot_mapping,

@@ -1,8 +1,10 @@
 """The row calls and calls over int8 pools without a GPU: sizes whose products leave their integers, tensors of another device,
 empty batches, and a step that checked mode refuses."""
 import pytest
+import torch
 
 import paged_kv_cache_409_b200 as pkv
+from test_binding_marshalling import mock  # noqa: F401
 
 EINVAL, EUNSUPPORTED = -1, -2
 P = 1 << 20
@@ -59,3 +61,28 @@ print('refused')
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=200)
     assert r.returncode == 0 and "refused" in r.stdout, (r.returncode, r.stdout + r.stderr)
+
+
+class Elsewhere(torch.Tensor):
+    """A tensor that says it lies on another device than the call's other ones."""
+
+    def get_device(self):
+        return 5
+
+
+def test_pools_of_another_device_are_refused(mock):  # noqa: F811
+    T, Hq, H, D = 2, 4, 2, 64
+    q, k, i = torch.zeros(T, Hq, D).half(), torch.zeros(T, H, D).half(), torch.zeros(T, dtype=torch.int64)
+    for call, pool, tail in ((pkv.rope_and_cache, torch.zeros(4, 16, H, D).half(), ()),
+                             (pkv.rope_and_cache_fp8, torch.zeros(4, 16, H, D, dtype=torch.uint8), (1.0, 1.0)),
+                             (pkv.rope_and_cache_int8, torch.zeros(4, 16, H, D + 4, dtype=torch.uint8), ())):
+        call(q, q, k, k, None, None, pool, pool, i, *tail)
+        for pools in ((pool.as_subclass(Elsewhere), pool), (pool, pool.as_subclass(Elsewhere))):
+            with pytest.raises(ValueError):
+                call(q, q, k, k, None, None, *pools, i, *tail)
+        for bad in (dict(cos_sin=torch.zeros(9, 32).as_subclass(Elsewhere), positions=i),
+                    dict(cos_sin=torch.zeros(9, 32), positions=i.as_subclass(Elsewhere)),
+                    dict(cos_sin=None, positions=None, q_norm_weight=torch.zeros(D).half().as_subclass(Elsewhere))):
+            with pytest.raises(ValueError):
+                call(q, q, k, k, key_cache=pool, value_cache=pool, slot_mapping=i, **bad,
+                     **dict(zip(("k_scale", "v_scale"), tail)))
