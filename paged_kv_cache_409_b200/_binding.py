@@ -624,20 +624,21 @@ def _rope_and_cache(fn, query_out, query, key, value, cos_sin, positions, dev, k
         fine = (cos_sin.dtype == _FLOAT32 and cos_sin.dim() == 2 and cos_sin.get_device() == dev and cos_sin.is_contiguous()
                 and positions is not None and positions.dtype == _INT64 and positions.shape == (T,)
                 and positions.get_device() == dev and positions.is_contiguous())
-        if fine:
-            max_position, rotary_dim = cos_sin.shape
-            table, pos = cos_sin.data_ptr(), positions.data_ptr()
-    weights = (qw, kw)
     if fine and qw is not None:
         fine = qw.dtype == dtype and qw.shape == (D,) and qw.get_device() == dev and qw.is_contiguous()
-        qw = qw.data_ptr()
     if fine and kw is not None:
         fine = kw.dtype == dtype and kw.shape == (D,) and kw.get_device() == dev and kw.is_contiguous()
-        kw = kw.data_ptr()
-    if not fine:
-        why = _rope_refusal(query_out, query, key, value, cos_sin, positions, dev, pool_shape, slot_mapping, weights)
+    if not fine:  # (an empty batch whose rows have odd strides has no reason)
+        why = _rope_refusal(query_out, query, key, value, cos_sin, positions, dev, pool_shape, slot_mapping, (qw, kw))
         if why:
             raise ValueError(why)
+    if cos_sin is not None:
+        max_position, rotary_dim = cos_sin.shape
+        table, pos = cos_sin.data_ptr(), positions.data_ptr()
+    if qw is not None:
+        qw = qw.data_ptr()
+    if kw is not None:
+        kw = kw.data_ptr()
     if T <= 1:  # a single row's token stride says nothing
         qs, ks = Hq * D, Hkv * D
         vs = ks

@@ -86,3 +86,15 @@ def test_pools_of_another_device_are_refused(mock):  # noqa: F811
             with pytest.raises(ValueError):
                 call(q, q, k, k, key_cache=pool, value_cache=pool, slot_mapping=i, **bad,
                      **dict(zip(("k_scale", "v_scale"), tail)))
+
+
+def test_an_empty_batch_of_any_layout_passes(mock):  # noqa: F811
+    """No token: whatever the strides of the empty rows are, with tables and weights given."""
+    Hq, H, D = 4, 2, 64
+    q, k, i = torch.zeros(0, D, Hq).half().transpose(1, 2), torch.zeros(0, D, H).half().transpose(1, 2), torch.zeros(0, dtype=torch.int64)
+    pool, w, table = torch.zeros(4, 16, H, D).half(), torch.zeros(D).half(), torch.zeros(9, 32)
+    pkv.rope_and_cache(torch.zeros(0, Hq, D).half(), q, k, k, table, i, pool, pool, i, q_norm_weight=w, k_norm_weight=w)
+    name, a = mock.last()
+    assert name == "pkv_rope_and_cache"
+    assert (a["num_tokens"], a["q_norm_weight"], a["k_norm_weight"], a["cos_sin"], a["rotary_dim"], a["max_position"]) == (
+        0, w.data_ptr(), w.data_ptr(), table.data_ptr(), 32, 9)
