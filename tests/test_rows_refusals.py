@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import paged_kv_cache_409_b200 as pkv
+from paged_kv_cache_409_b200 import _binding
 from test_binding_marshalling import mock  # noqa: F401
 
 EINVAL, EUNSUPPORTED = -1, -2
@@ -70,7 +71,8 @@ class Elsewhere(torch.Tensor):
         return 5
 
 
-def test_pools_of_another_device_are_refused(mock):  # noqa: F811
+def test_pools_of_another_device_are_refused(mock, monkeypatch):  # noqa: F811
+    monkeypatch.setattr(_binding, "_current_device", lambda: 0)
     T, Hq, H, D = 2, 4, 2, 64
     q, k, i = torch.zeros(T, Hq, D).half(), torch.zeros(T, H, D).half(), torch.zeros(T, dtype=torch.int64)
     for call, pool, tail in ((pkv.rope_and_cache, torch.zeros(4, 16, H, D).half(), ()),
