@@ -163,3 +163,38 @@ def test_every_finite_fp16_row_is_taken():
             pkv.reshape_and_cache_int8(k.half(), v.half(), kp, vp, (bt[0, pos // 16].long() * 16 + pos % 16).view(1))
         q = torch.randn(41, 2, D, device="cuda").half()
         compare(q, kp, vp, bt, ns, lens, 1e-4, "rows of 65504")
+
+
+def test_bad_chunk_offsets_leave_the_other_chunks_alone():
+    """Offsets that run backwards, with no row in two chunks: the chunk of negative length is flagged and writes nothing, the
+    others' rows are what they are without it, and rows of no chunk stay as they were."""
+    kp, vp, bt = make_pools([60, 30, 90], 16, 2, 64, seed=23)
+    q = torch.randn(70, 4, 64, device="cuda").half()
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def run(offsets, lens):
+        out = torch.full_like(q, 7.0)
+        pkv.paged_attention_prefill_chunk_int8(out, q, kp, vp, bt[: len(lens)], i32(*lens), i32(*offsets), 40, 0.1)
+        return out, pkv.get_device_error()
+
+    for offsets, lens, rows, bad in (([0, 20, 10, 10], [60, 30, 90], [(0, 0, 20)], 1), ([20, 10, 40, 50], [60, 30, 90],
+                                                                                     [(1, 10, 40), (2, 40, 50)], 0)):
+        out, err = run(offsets, lens)
+        assert err == pkv._binding.DEVERR_LENGTH
+        written = torch.zeros(70, dtype=torch.bool, device="cuda")
+        for chunk, lo, hi in rows:
+            written[lo:hi] = True
+            ref, bound = reference(q[lo:hi], kp, vp, bt[chunk], lens[chunk],
+                                   torch.arange(lens[chunk] - (hi - lo), lens[chunk], device="cuda"), 0.1, q.dtype)
+            check(out[lo:hi], ref, bound, f"offsets {offsets} chunk {chunk}")
+        assert bool((out[~written] == 7.0).all())
+
+
+def test_wide_tables():
+    """Tables far wider than the contexts: the same rows."""
+    ns, lens = [70, 3, 1], [300, 60, 1]
+    kp, vp, bt = make_pools(lens, 16, 2, 128, seed=29)
+    q = torch.randn(sum(ns), 8, 128, device="cuda").bfloat16()
+    wide = torch.full((3, 8192), -1, dtype=torch.int32, device="cuda")
+    wide[:, : bt.shape[1]] = bt
+    compare(q, kp, vp, wide, ns, lens, 0.09, "table for 131072 tokens")
