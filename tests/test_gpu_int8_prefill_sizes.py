@@ -198,3 +198,23 @@ def test_wide_tables():
     wide = torch.full((3, 8192), -1, dtype=torch.int32, device="cuda")
     wide[:, : bt.shape[1]] = bt
     compare(q, kp, vp, wide, ns, lens, 0.09, "table for 131072 tokens")
+
+
+@pytest.mark.parametrize("Hkv", [1, 8, 30])
+@pytest.mark.parametrize("cols", [129, 1000, 8192])
+def test_wide_tables_with_items_of_every_length(cols, Hkv):
+    """Clusters chosen for a table's width, with items from one key tile on; the same bits twice, and a
+    NaN query row shows in its own row alone."""
+    ns, lens = [1, 130, 3, 200, 64], [1, 130, 700, 1500, 2060]
+    kp, vp, bt = make_pools(lens, 16, Hkv, 64, seed=31)
+    wide = torch.full((5, max(cols, bt.shape[1])), -1, dtype=torch.int32, device="cuda")
+    wide[:, : bt.shape[1]] = bt
+    q = torch.randn(sum(ns), 2 * Hkv, 64, device="cuda").half()
+    compare(q, kp, vp, wide, ns, lens, 0.125, f"tables of {cols}")
+    out = prefill(q, kp, vp, wide, ns, lens, 0.125)
+    assert torch.equal(out, prefill(q, kp, vp, wide, ns, lens, 0.125))
+    q[140, 0, 5] = float("nan")
+    nan = prefill(q, kp, vp, wide, ns, lens, 0.125)
+    assert bool(torch.isnan(nan[140, 0]).all())
+    nan[140, 0] = out[140, 0]
+    assert torch.equal(nan, out)
