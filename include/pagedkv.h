@@ -65,7 +65,11 @@ typedef enum { PKV_F32 = 0, PKV_F16 = 1, PKV_BF16 = 2, PKV_FP8_E4M3 = 3 } pkv_dt
  * all, so pkv_copy_blocks and pkv_swap_blocks move whole blocks with that
  * block_bytes.  s is at least 2^-80 (smaller rows are coded with that step, a
  * zero row's codes are 128); a row that holds a NaN or an infinity gets the
- * scale NaN (its codes are then unspecified) and reads as NaN. */
+ * scale NaN (its codes are then unspecified) and reads as NaN.
+ * Rows of any head_dim that is a multiple of 16, up to 256, can be written and
+ * read back; the attention calls take head_dim 64 and 128, block_size 8, 16 and
+ * 32, and 1, 2, 4 or 8 query heads per KV head, so other int8 pools cannot be
+ * attended.  Codes are 1 to 255. */
 #define PKV_INT8 4
 
 typedef enum {
@@ -235,7 +239,8 @@ int64_t pkv_int8_block_bytes(int block_size, int num_kv_heads, int head_dim);
 /* Write new tokens' K and V rows into int8 pools, quantising on the way.
  * Arguments as for pkv_reshape_and_cache_fp8 without the scales; the pools are
  * num_blocks blocks of pkv_int8_block_bytes.  head_dim: a multiple of 16, at
- * most 256; block_size * num_kv_heads a multiple of 4. */
+ * most 256; block_size * num_kv_heads a multiple of 4.  Two tokens with the same
+ * slot race: the row may be left with codes of one and the scale of the other. */
 int pkv_reshape_and_cache_int8(const void* key, const void* value, void* key_cache, void* value_cache,
                                const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads, int head_dim,
                                int block_size, int64_t num_blocks, int src_dtype, pkv_stream_t stream);
@@ -363,7 +368,10 @@ int pkv_paged_attention_decode_fp8(void* out, const void* query, const void* key
  * pkv_paged_attention_decode with every pool row read as its scale times
  * (code - 128).  The query is used as a 16-bit integer row (half a step is
  * 2^-16 of its largest element); products with the codes are exact, weights
- * are f16 relative to the largest weight times V scale, sums are fp32.
+ * are f16 relative to the largest weight times V scale, sums are fp32.  (The
+ * weight of a V row is formed times its scale in fp32: where scales of one
+ * context differ by more than 2^100, which fp16 rows cannot, a row of the
+ * smallest may lose its share of the softmax sum.)
  *
  *   query, out      device [num_seqs, num_q_heads, head_dim], dtype F16 or BF16
  *   key_cache,
@@ -526,7 +534,10 @@ int pkv_paged_attention_prefill_chunk_fp8(void* out, const void* query, const vo
  * decode takes such larger rows).
  * Supported: dtype in {F16, BF16}, head_dim in {64, 128}, block_size in {8, 16,
  * 32}, num_q_heads / num_kv_heads in {1, 2, 4, 8}.  Everything else is as
- * there; the same call verifies a few draft tokens per sequence.
+ * there; the same call verifies a few draft tokens per sequence.  With few
+ * items of work (pairs of 128-row query tiles, chunks, KV heads) several CTAs share
+ * one, as many as pay for a context of the table's width, max_blocks_per_seq *
+ * block_size: give a table as narrow as the longest context.
  */
 int pkv_paged_attention_prefill_chunk_int8(void* out, const void* query, const void* key_cache,
                                            const void* value_cache, const int32_t* block_tables,

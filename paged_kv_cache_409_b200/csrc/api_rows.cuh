@@ -52,7 +52,9 @@ int rows_int8_check(const void* x, const void* y, const void* key_cache, const v
 // it in the stream: its CTAs are set up while that kernel drains, and the first
 // thing they do is wait for its completion (griddepcontrol.wait).  Only then do
 // they let a dependent of their own (a step's decode) start, so that one never
-// runs beside anything but this kernel.
+// runs beside anything but this kernel.  The wait covers that one kernel; what lies
+// before it is done because every kernel here that is a dependent launch itself
+// waits in each of its grids, whatever the data.
 template <typename P>
 int launch_after(void (*kern)(P), dim3 grid, cudaStream_t s, const std::remove_const_t<P>& p) {
     return launch_kernel(kern, grid, dim3(128), 0, Launch{s, true}, p);
@@ -148,7 +150,11 @@ int launch_read(const pkv::ReadRowsParams& p, cudaStream_t s) {
 // part, 202 in two).  fit[k]: clusters of k CTAs that run at once; a GPC's SMs
 // limit it (15 of eight, 22 of six: 16 items of 16128 keys take 108 us in
 // eight parts, whose last cluster runs alone, and 68 in six).  The lengths are
-// not known here: max_tiles is the table's reach.
+// not known here: max_tiles is the table's reach, so tables far wider than the
+// contexts cut items that are better whole (19 chunks of 64 rows over 1024 keys,
+// 8 KV heads: 60 us with tables of 1056 tokens, 103 with 8192 or more).  Letting
+// CTAs that a short item does not need leave at once does not help (97 us): their
+// SMs go to no other cluster until theirs is done.
 int prefill_parts(int64_t items, int64_t max_tiles, const int (&fit)[9]) {
     auto cost = [&](int parts) {
         const double waves = (double)items / fit[parts];

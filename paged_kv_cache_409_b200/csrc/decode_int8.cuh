@@ -31,7 +31,8 @@
 // same barrier.
 //
 // Bound by memory.  64 sequences of [128, 2048] tokens x 32 heads of 128, fp16:
-// 92-94 us, 6.4 TB/s (0.98 of a copy).  256 sequences x 8 KV heads, 8 query heads
+// 92-94 us in graph replays over three sets of inputs, 6.4 TB/s (0.98 of a copy);
+// 93-99 us as a call on new inputs.  256 sequences x 8 KV heads, 8 query heads
 // each: 118-128 us, 5.7-6.2 TB/s; there the eight columns of an MMA are all in
 // use, and what is left is the ranking and the last wave.  Four warps of two
 // stages and units of 16 tokens: 8 warps, 2 warps, 3 stages and units of 32 are
@@ -114,7 +115,11 @@ struct DecodeInt8Cfg {
 // first: lengths fall into 32 classes (len >> shift, shift chosen for the call's
 // bound), sequences of one class keep their order.  Every CTA finds its own: a
 // histogram and a scan give the class, ballots the place in it.  No CTA then
-// starts a long sequence last.
+// starts a long sequence last.  Up to 256 sequences, two lengths a thread; larger
+// batches go in the listed order and by the other pools' split rule, which costs
+// most just behind the limit and nothing further on (lognormal lengths up to
+// 4096, 64 heads over 8: 256 sequences 120 us, 6.0 TB/s; 257 135, 5.3; 300 154,
+// 5.5; 512 252, 5.9; 1024 510, 5.9).
 constexpr int kMaxRankedSeqs = 256;
 
 template <int kThreads>
@@ -163,12 +168,12 @@ __device__ __forceinline__ int sequence_by_length(const int32_t* lens, int n, in
     return found;
 }
 
-// CTAs per SM that the registers are told to allow.  Four (106-124 registers,
-// where the compiler by itself takes 96-98 at head dim 128 and 64-95 at 64) gain
-// up to 5 % where an MMA's columns are in use (256 sequences, 8 query heads each
-// of 128: 128 against 130 us; 4 heads, 128 sequences over [512, 4096]: 99 against
-// 104) and lose as much elsewhere (64 sequences x 32 heads of 128: 99 against 94
-// us; 8 query heads of 64: 62 against 58).
+// CTAs per SM that the registers are told to allow: four (106-124 registers) where
+// that is faster than what the compiler takes by itself (96-98 at head dim 128,
+// 64-95 at 64).  us, by itself | four, of 128 sequences over [512, 4096], blocks of
+// 16, 16 KV heads for 1 and 2 query heads each, 8 for 4 and 8:
+//   head dim 128: 184.0 | 185.7, 190.1 | 193.6, 102.3 | 99.1, 111.9 | 107.4
+//   head dim 64:  109.8 | 109.9, 109.0 | 107.3, 51.6 | 51.1, 51.9 | 53.8
 constexpr int int8_min_ctas(int D, int G) { return (D == 128 ? G >= 4 : G < 8) ? 4 : 0; }
 
 template <typename T, int D, int B, int G, int NST, int NW, int U>

@@ -435,7 +435,8 @@ int decode_fp8_by_block(int block_size, int group, const pkv::DecodeParams& prm,
 // int8 pools: two stages per warp, each a unit of blocks.  Units have at least
 // 16 tokens; 32 with 64-byte rows, where 16 make only a kilobyte per copy
 // (blocks of 16: 127 -> 103, 136 -> 107, 66 -> 51, 58 -> 57 us for 1, 2, 4, 8
-// query heads per KV head, 128 sequences over [512, 4096]), except with blocks
+// query heads per KV head, 128 sequences over [512, 4096], 16 KV heads for 1 and
+// 2, 8 for 4 and 8), except with blocks
 // of 8 and few heads, whose units would take 16 copies (118 -> 122, 108 -> 117,
 // but 61 -> 54 and 64 -> 57 with 4 and 8 heads).  With 128-byte rows units of 32
 // take 0-15 % longer, and units of 64 lose everywhere.
