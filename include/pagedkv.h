@@ -523,15 +523,20 @@ int pkv_paged_attention_prefill_chunk_fp8(void* out, const void* query, const vo
 /*
  * Chunked prefill over int8 pools: pkv_paged_attention_prefill_chunk with every
  * pool row read as its scale times (code - 128).  The rows are widened inside
- * the kernel, to f16: no workspace.  Both products run in f16 with fp32
- * accumulation, in units that put the largest rows near f16's largest value: an
- * element is rounded by half a step, 2^-11 of it, or by less than 2^-35 of the
- * largest K row of its 128 keys, or V row up to them (so rows of any size are
- * taken alike, if those seen together lie within 2^25 of one another).  A bf16
- * query row is narrowed in a unit of its own, exactly down to 2^-28 of its largest
- * element.  A row whose scale is NaN, or that holds more than fp16's largest
- * value, 65504, gives NaN to the query rows that see it, and to no others (the
- * decode takes such larger rows).
+ * the kernel: no workspace.  Both products run in f16 with fp32 accumulation.
+ *   F16    the codes are the operands, exactly; scales are applied in fp32, and
+ *          a weight times its V row's scale is rounded to f16 (2^-11 of it), as in
+ *          the decode, rows of any size alike.
+ *   BF16   the rows are rounded to f16 (2^-11 of an element) in units that put the
+ *          largest near f16's largest value; what f16 loses below its range is less
+ *          than 2^-35 of the largest K row of the element's 128 keys, or of the
+ *          largest V row up to them: rows of any size are taken alike, if those
+ *          seen together lie within 2^25 of one another.  A query row is narrowed in
+ *          a unit of its own, exactly down to 2^-28 of its largest element.  A row
+ *          that holds more than fp16's largest value, 65504, counts as NaN (the
+ *          decode, and F16 here, take such rows).
+ * A row whose scale is NaN gives NaN to the query rows that see it, and to no
+ * others.
  * Supported: dtype in {F16, BF16}, head_dim in {64, 128}, block_size in {8, 16,
  * 32}, num_q_heads / num_kv_heads in {1, 2, 4, 8}.  Everything else is as
  * there; the same call verifies a few draft tokens per sequence.  With few

@@ -4,12 +4,23 @@
 // K and V tiles widened in shared memory by warps of their own, so that the
 // cache is read once, as it lies, and no scratch is needed.
 //
-// Widening.  Tile rows arrive as codes (16 KB at head_dim 128) with one fp32
-// scale each.  A converter thread turns four codes into two f16 pairs: a byte
-// permute puts 0x48 over each code (8 + u / 128), a subtraction of 9 leaves
-// c = (u - 128) / 128 exactly, and the element is c * hi + c * lo with S, 128
-// times the scale in the units below, split in two f16 parts (2^-22 of it), so that
-// what is rounded is the product: 2^-11 of the element.
+// fp16 queries: exact codes.  Tile rows arrive as codes (16 KB at head_dim 128)
+// with one fp32 scale each.  A converter thread turns four codes into two f16 pairs:
+// a byte permute puts 0x64 over each code (1024 + u), a subtraction of 1152 leaves
+// u - 128 exactly.  The scales go into the softmax, as in decode_int8.cuh: K's
+// multiplies its column of S, the logarithm of V's is added to the exponent, and
+// the sum takes each weight over V's scale.  So P is near 1 for the largest
+// product whatever the rows' sizes are, and only P and the result are rounded: an
+// fp16 result is off by 2.6-2.9e-4 of its norm against 64 bits, where an fp32 form
+// rounded once is off by 2.1e-4 and elements rounded to f16 (below) come to
+// 4.7-7.0e-4.  Three 16-byte reads and two packed FMAs more for four scores: four
+// chunks of 512 rows (below) 206 us against 168, seven ragged ones 22.9 against 22.1.
+//
+// bf16 queries: elements rounded to f16, whose error (2^-11 of an element) is well
+// below the result's own rounding (2^-8).  A byte permute puts 0x48 over a code (8 +
+// u / 128), a subtraction of 9 leaves c = (u - 128) / 128 exactly, and the element is
+// c * hi + c * lo with S, 128 times the scale in the units below, split in two f16
+// parts (2^-22 of it), so that what is rounded is the product.
 // Units.  f16 keeps those 11 bits over 30 binades only, and rows may be of any
 // size: rows of 1e-4 taken as they are came out 4 % off (the split itself fell
 // on the subnormal grid), rows of 3e-6 as zeros.  So the loader, which has a
@@ -18,13 +29,14 @@
 // one, 2^12 or above for the largest row so far, which only grows: the scores
 // are multiplied back with the scale they take anyway, and O is rescaled, as for
 // a new maximum, in the few tiles where V's unit grows.  An f16 subnormal is then
-// below 2^-35 of the largest such row.  bf16 query rows are narrowed in units of
-// their own likewise.  All of it costs the softmax one 16-byte read and two
+// below 2^-35 of the largest such row.  Query rows are narrowed in units of their
+// own likewise.  All of it costs the softmax one 16-byte read and two
 // multiplications a tile.
-// Rows past the sequence and rows of bad blocks are written as zeros: P is zero
-// there, and 0 * NaN must not reach O.  For the same reason a V row whose scale is
-// NaN (or beyond f16's largest value / 127) becomes zeros and its K row NaN: the
-// scores that see the row are NaN, those that the causal mask hides stay out of it.
+//
+// Rows past the sequence and those of bad blocks have finite tile elements (bf16:
+// zeros), since 0 * NaN must not reach O.  For the same reason a row of scale NaN
+// (bf16: or beyond f16's largest value / 127) shows in its scores alone, K and V
+// rows both: those that the causal mask hides stay out of it.
 //
 // Roles (512 threads; the registers of the second half go to the softmax):
 //   warps 0-7   softmax, four per query tile, as in prefill.cuh; with bf16
@@ -32,6 +44,8 @@
 //   warp 8      loader: Q tiles, then the codes and scales of K_j and V_j into
 //               one staging buffer each, refilled when it has been widened
 //   warp 9      MMA issue
+//   warp 10     fp16: what the softmax takes of the scales, a tile ahead (K's factors
+//               and V's logarithms in two stages, V's inverses, read last, in one)
 //   warps 12-15 converters: staging -> f16 K (two stages) and V (two stages)
 // Every wait is bounded, as in prefill.cuh.
 //
@@ -43,7 +57,7 @@
 //
 // Bound by the chain of a query tile's steps (S, softmax, P.V: 2.25 us per 128
 // keys for two tiles, of which the tensor cores work 1.5): four chunks of 512
-// rows over up to 8446 keys, 32 query heads on 8 KV heads of 128, 166 us, 705
+// rows over up to 8446 keys, 32 query heads on 8 KV heads of 128, bf16, 167 us, 701
 // TFLOP/s (0.43 of the bf16 rate), set by the items of 66 key tiles.  In the
 // chain it is the softmax threads' issue slots and latency that count, not the
 // exponential unit: a polynomial for an eighth, a quarter, half of the
@@ -71,6 +85,7 @@ constexpr int kPrefillInt8Threads = 512;
 #ifndef PKV_PREFILL_CONV_REGS
 #define PKV_PREFILL_CONV_REGS 64  // registers of the second half's threads; the softmax gets 256 minus this
 #endif
+constexpr int kPrefillInt8ScaleWarp = 10;  // fp16 queries
 constexpr int kPrefillInt8ConvWarp = 12;   // first of four
 constexpr int kPrefillInt8ConvThreads = 128;
 
@@ -86,11 +101,14 @@ struct PrefillInt8Cfg {
     static constexpr int V_OFF = K_OFF + 2 * KT_BYTES;   // [2] stages
     static constexpr int KC_OFF = V_OFF + 2 * KT_BYTES;  // staging of K, then of V
     static constexpr int VC_OFF = KC_OFF + C_BYTES;
-    static constexpr int SC_OFF = VC_OFF + C_BYTES;      // scales: K [BN], V [2][BN] (tile j in j & 1)
-    static constexpr int UNIT_OFF = SC_OFF + 3 * BN * 4;  // [4] units of tile j in j & 3
-    static constexpr int BAR_OFF = UNIT_OFF + 4 * 16;
-    static constexpr int NBAR = 28;
-    static constexpr int SMEM = 1024 + BAR_OFF + NBAR * 8;
+    // scales.  bf16: K [BN], V [2][BN] (tile j in j & 1), and the units of tile j
+    // [4] in j & 3; fp16: K's factors [2][BN], log2 of V's [2][BN], V's inverses [BN]
+    static constexpr int SC_OFF = VC_OFF + C_BYTES;
+    static constexpr int UNIT_OFF = SC_OFF + 3 * BN * 4;
+    static constexpr int IV_OFF = SC_OFF + 4 * BN * 4;
+    static constexpr int BAR_OFF = SC_OFF + 5 * BN * 4;
+    static constexpr int NBAR = 33;
+    static constexpr int SMEM = BAR_OFF + NBAR * 8;
     static constexpr uint32_t TMEM_COLS = 512, S_COL0 = 0, O_COL0 = 256;
     static_assert(SMEM <= 227 * 1024, "shared memory");
     // the cluster's merge: O [256][D] in fp32 (16-byte chunks swizzled by row), then (max, sum) per row
@@ -168,6 +186,11 @@ __device__ __forceinline__ uint2 widen_codes4(uint32_t u, uint32_t s_hi, uint32_
     return make_uint2(hfma2_u(a, s_hi, hmul2_u(a, s_lo)), hfma2_u(b, s_hi, hmul2_u(b, s_lo)));
 }
 
+// Four codes as u - 128.
+__device__ __forceinline__ uint2 exact_codes4(uint32_t u) {
+    return make_uint2(hsub2_1152(__byte_perm(u, 0x64646464u, 0x4140)), hsub2_1152(__byte_perm(u, 0x64646464u, 0x4342)));
+}
+
 // T: the query's and output's type; the MMAs run in f16.
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
@@ -176,10 +199,10 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
     using C = PrefillInt8Cfg<D, G>;
     const PrefillParams& p = prm.base;
     const int B = p.block_size;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = align_1024(smem_raw);
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
     constexpr bool kNarrowQ = Elem<T>::kCuType == CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    constexpr bool kExact = !kNarrowQ;  // the tiles hold the codes, the softmax takes the scales
     uint64_t* q_full = bars + 0;
     uint64_t* q_ready = bars + 1;   // Q tiles in f16 (256 arrivals; bf16 queries)
     uint64_t* c_full = bars + 2;    // [2] codes of K and both scales | codes of V landed
@@ -194,7 +217,11 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
     uint64_t* mma_done = bars + 20;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 22);
-    uint64_t* u_full = bars + 23;   // [4] units of tile j written, in j & 3
+    uint64_t* u_full = bars + 23;   // [4] units of tile j written, in j & 3 (bf16)
+    uint64_t* f_full = bars + 23;   // [2] K's factors and V's logarithms of tile j written, in j & 1 (fp16)
+    uint64_t* f_free = bars + 25;   // [2][2] per query tile: read (4 arrivals)
+    uint64_t* i_full = bars + 29;   // V's inverses of tile j written (fp16)
+    uint64_t* i_free = bars + 30;   // [2] per query tile: read (4 arrivals)
 
     griddep_wait();  // launched as a dependent of whatever comes before it
     const int parts = cluster_size(), rank = cluster_rank();
@@ -252,7 +279,17 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
             mbar_init(&p_full[i], 128);
             mbar_init(&o_full[i], 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&u_full[i], 1);
+        if constexpr (kExact) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&f_full[i], 1);
+                mbar_init(&f_free[i], 4);
+                mbar_init(&f_free[2 + i], 4);
+                mbar_init(&i_free[i], 4);
+            }
+            mbar_init(i_full, 1);
+        } else {
+            for (int i = 0; i < 4; ++i) mbar_init(&u_full[i], 1);
+        }
         mbar_init(mma_done, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -267,29 +304,39 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
     // 256 * 192 + 256 * 64 = 512 * 128.
     if (warp >= 8) {
         regs_dec<PKV_PREFILL_CONV_REGS>();
+        // For the warps that follow the block table.  Block ids of this CTA's key
+        // tile j, one per lane; read one tile ahead.
+        const int lane = tid & 31;
+        const int per_tile = C::BN / B;  // blocks per key tile (4..16)
+        auto fetch_ids = [&](int j) -> int {
+            const int lb = (tb + j) * per_tile + lane;
+            return (lane < per_tile && lb < nblk) ? bt_row[lb] : -1;
+        };
+        // Ids checked when they arrive; -1: nothing to load (the tiles behind
+        // this CTA's last are another's to check and flag).
+        auto checked_ids = [&](int j, int id, bool flag) -> int {
+            if (lane >= per_tile || j >= nkt || (tb + j) * per_tile + lane >= nblk) return -1;
+            if (id >= 0 && id < p.num_blocks) return id;
+            if (flag) flag_error(PKV_DEVERR_BLOCK_ID);
+            return -1;
+        };
+        // The tile's scales, four K and four V rows per lane, into registers a
+        // tile ahead of their use (copies of 32 to 128 bytes each would cost as
+        // many bulk copies as the codes); rows of blocks that are not loaded
+        // get 0: zeros.
+        auto fetch_scales = [&](int id, float4& ks, float4& vs) {
+            const int own = __shfl_sync(0xffffffffu, id, 4 * lane / B);
+            ks = vs = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (own >= 0) {
+                const int64_t off = own * prm.block_bytes + (g * B + (4 * lane) % B) * 4;
+                ks = *reinterpret_cast<const float4*>(prm.k_scales + off);
+                vs = *reinterpret_cast<const float4*>(prm.v_scales + off);
+            }
+        };
         if (warp == kPrefillLoadWarp) {
             // ============================================================ loader (whole warp, lane 0 issues)
-            const int lane = tid & 31;
             const bool leader = lane == 0;
-            const int per_tile = C::BN / B;  // blocks per key tile (4..16)
             float* scales = reinterpret_cast<float*>(smem + C::SC_OFF);
-            // Block ids of this CTA's key tile j, one per lane; read one tile ahead.
-            auto fetch_ids = [&](int j) -> int {
-                const int lb = (tb + j) * per_tile + lane;
-                return (lane < per_tile && lb < nblk) ? bt_row[lb] : -1;
-            };
-            // Ids checked when they arrive; -1: nothing to load (the tiles behind
-            // this CTA's last are another's to check and flag).
-            auto checked_ids = [&](int j, int id) -> int {
-                if (lane >= per_tile || j >= nkt || (tb + j) * per_tile + lane >= nblk) return -1;
-                if (id >= 0 && id < p.num_blocks) return id;
-                flag_error(PKV_DEVERR_BLOCK_ID);
-                return -1;
-            };
-            // The tile's scales, four K and four V rows per lane, into registers a
-            // tile ahead of their use (copies of 32 to 128 bytes each would cost as
-            // many bulk copies as the codes); rows of blocks that are not loaded
-            // get 0: zeros.
             // The largest scale a row may have: fp16's largest value / 127, and what
             // the rounding of a scale adds.
             constexpr float kMaxScale = 65504.f / 127.f * (1.f + 0x1p-20f);
@@ -323,15 +370,6 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
                 vs4 = make_float4(vs[0] * vm, vs[1] * vm, vs[2] * vm, vs[3] * vm);
                 return make_float4(pow2(k_unit - 7), pow2(v_unit - 5), grown, 0.f);
             };
-            auto fetch_scales = [&](int id, float4& ks, float4& vs) {
-                const int own = __shfl_sync(0xffffffffu, id, 4 * lane / B);
-                ks = vs = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (own >= 0) {
-                    const int64_t off = own * prm.block_bytes + (g * B + (4 * lane) % B) * 4;
-                    ks = *reinterpret_cast<const float4*>(prm.k_scales + off);
-                    vs = *reinterpret_cast<const float4*>(prm.v_scales + off);
-                }
-            };
             // The codes of a tile, K (0) or V (1): lane i copies block i.
             auto load_codes = [&](int which, const CUtensorMap* map, int id) {
                 if (leader) mbar_arrive_expect_tx(&c_full[which], C::C_BYTES);
@@ -352,32 +390,34 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
                                     q0 + (qt0 + x) * C::TT, q_full);
                 }
             }
-            int ids = checked_ids(0, fetch_ids(0));
+            int ids = checked_ids(0, fetch_ids(0), true);
             int ids_next = fetch_ids(1);
-            float4 ks, vs;
-            fetch_scales(ids, ks, vs);
+            float4 ks, vs, units;
+            if constexpr (!kExact) fetch_scales(ids, ks, vs);
             int loaded_k = 0, loaded_v = 0;
             for (int j = 0; j < nkt; ++j) {
                 const int ids_later = fetch_ids(j + 2);
-                const float4 units = scale_units(j, ks, vs);
+                if constexpr (!kExact) units = scale_units(j, ks, vs);
                 if (j > 0 && !__all_sync(0xffffffffu, mbar_wait_or_abort_idle(&c_free[0], (j - 1) & 1, abort_flag))) break;
-                *reinterpret_cast<float4*>(scales + 4 * lane) = ks;
-                *reinterpret_cast<float4*>(scales + (1 + (j & 1)) * C::BN + 4 * lane) = vs;
-                // Read by the softmax threads of tile j, which are done with it before
-                // S(j + 1) runs, whose K stage tile j + 3 is widened into: j + 4 may
-                // overwrite it.
-                if (leader) {
-                    *reinterpret_cast<float4*>(smem + C::UNIT_OFF + (j & 3) * 16) = units;
-                    mbar_arrive(&u_full[j & 3]);
+                if constexpr (!kExact) {
+                    *reinterpret_cast<float4*>(scales + 4 * lane) = ks;
+                    *reinterpret_cast<float4*>(scales + (1 + (j & 1)) * C::BN + 4 * lane) = vs;
+                    // Read by the softmax threads of tile j, which are done with it before
+                    // S(j + 1) runs, whose K stage tile j + 3 is widened into: j + 4 may
+                    // overwrite it.
+                    if (leader) {
+                        *reinterpret_cast<float4*>(smem + C::UNIT_OFF + (j & 3) * 16) = units;
+                        mbar_arrive(&u_full[j & 3]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
                 load_codes(0, &tm_k, ids);
                 loaded_k = j + 1;
                 if (j > 0 && !__all_sync(0xffffffffu, mbar_wait_or_abort_idle(&c_free[1], (j - 1) & 1, abort_flag))) break;
                 load_codes(1, &tm_v, ids);
                 loaded_v = j + 1;
-                ids = checked_ids(j + 1, ids_next);
-                fetch_scales(ids, ks, vs);
+                ids = checked_ids(j + 1, ids_next, true);
+                if constexpr (!kExact) fetch_scales(ids, ks, vs);
                 ids_next = ids_later;
             }
             if (leader) {
@@ -455,6 +495,44 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
                 umma_commit(mma_done);  // every MMA done before tensor memory is released
                 mbar_wait(mma_done, 0);
             }
+        } else if (kExact && warp == kPrefillInt8ScaleWarp) {
+            // ============================================================ scales (fp16): what the softmax takes of them
+            float* factors = reinterpret_cast<float*>(smem + C::SC_OFF) + 4 * lane;
+            int ids_next = fetch_ids(1);
+            float4 ks, vs;
+            fetch_scales(checked_ids(0, fetch_ids(0), false), ks, vs);
+            for (int j = 0; j < nkt; ++j) {
+                const int ids_later = fetch_ids(j + 2), st = j & 1;
+                float k[4] = {ks.x, ks.y, ks.z, ks.w}, v[4] = {vs.x, vs.y, vs.z, vs.w}, lg[4];
+                const int live = L - ((tb + j) * C::BN + 4 * lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    k[i] *= p.scale_log2;
+                    if (i >= live) k[i] = 0.f, v[i] = 1.f;
+                    // a row that is not finite shows in the scores alone
+                    if (!(abs_bits(k[i]) < 0x7f800000u && abs_bits(v[i]) < 0x7f800000u)) k[i] = __uint_as_float(0x7fc00000u), v[i] = 1.f;
+                    v[i] = fmaxf(v[i], kInt8MinScale);
+                    lg[i] = log2f(v[i]);
+                }
+                bool ok = true;
+                for (int x = 0; x < 2; ++x)
+                    if (j >= 2 && j - 2 < (x == 0 ? nka : nkb))
+                        ok = ok && mbar_wait_or_abort_idle(&f_free[2 * x + st], ((j - 2) >> 1) & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                *reinterpret_cast<float4*>(factors + st * C::BN) = make_float4(k[0], k[1], k[2], k[3]);
+                *reinterpret_cast<float4*>(factors + (2 + st) * C::BN) = make_float4(lg[0], lg[1], lg[2], lg[3]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&f_full[st]);
+                for (int x = 0; x < 2; ++x)
+                    if (j >= 1 && j - 1 < (x == 0 ? nka : nkb))
+                        ok = ok && mbar_wait_or_abort_idle(&i_free[x], (j - 1) & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                *reinterpret_cast<float4*>(smem + C::IV_OFF + 16 * lane) = make_float4(1.f / v[0], 1.f / v[1], 1.f / v[2], 1.f / v[3]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(i_full);
+                fetch_scales(checked_ids(j + 1, ids_next, false), ks, vs);
+                ids_next = ids_later;
+            }
         } else if (warp >= kPrefillInt8ConvWarp) {
             // ============================================================ converters
             const int ct = tid - kPrefillInt8ConvWarp * 32;
@@ -467,7 +545,7 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
             const int row = ct, sw = row & 7;
             auto widen = [&](int which, int j, uint8_t* dst) {
                 const uint8_t* src = smem + (which ? C::VC_OFF : C::KC_OFF);
-                const float s = scales[(which ? 1 + (j & 1) : 0) * C::BN + row];
+                const float s = kExact ? 0.f : scales[(which ? 1 + (j & 1) : 0) * C::BN + row];
                 const __half hi = __float2half_rn(s);
                 const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(__float2half_rn(s - __half2float(hi)));
                 const uint32_t sh = *reinterpret_cast<const uint32_t*>(&hi2);
@@ -477,8 +555,8 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
 #pragma unroll kUnroll
                 for (int ch = 0; ch < D / 16; ++ch) {
                     const uint4 u = *reinterpret_cast<const uint4*>(src + int8_chunk<D>(row, ch));
-                    const uint2 a = widen_codes4(u.x, sh, sl), b = widen_codes4(u.y, sh, sl);
-                    const uint2 c = widen_codes4(u.z, sh, sl), d = widen_codes4(u.w, sh, sl);
+                    auto widen4 = [&](uint32_t w) { return kExact ? exact_codes4(w) : widen_codes4(w, sh, sl); };
+                    const uint2 a = widen4(u.x), b = widen4(u.y), c = widen4(u.z), d = widen4(u.w);
                     uint8_t* panel = out + (ch / 4) * C::BN * 128;
                     const int v0 = 2 * (ch % 4);
                     *reinterpret_cast<uint4*>(panel + ((v0 ^ sw) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
@@ -560,15 +638,20 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
             }
         }
         for (int j = 0; ok && j < nk; ++j) {
-            if (!__all_sync(0xffffffffu, mbar_wait_or_abort(&u_full[j & 3], (j >> 2) & 1, abort_flag) &&
+            if (!__all_sync(0xffffffffu, mbar_wait_or_abort(kExact ? &f_full[j & 1] : &u_full[j & 3],
+                                                            (j >> (kExact ? 1 : 2)) & 1, abort_flag) &&
                                              mbar_wait_or_abort(&s_full[x], j & 1, abort_flag))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const float4 units = *reinterpret_cast<const float4*>(smem + C::UNIT_OFF + (j & 3) * 16);
-            const float sl2 = p.scale_log2 * (q_unit * units.x);
-            v_unit = units.y;
+            float sl2 = 1.f, grown = 1.f;
+            if constexpr (!kExact) {
+                const float4 units = *reinterpret_cast<const float4*>(smem + C::UNIT_OFF + (j & 3) * 16);
+                sl2 = p.scale_log2 * (q_unit * units.x);
+                v_unit = units.y;
+                grown = units.z;
+            }
             float sv[C::BN];
             {
                 uint32_t u[C::BN];
@@ -581,6 +664,18 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
             }
             const int k0 = (tb + j) * C::BN;
             const bool all_vis = k0 + C::BN - 1 <= qpos;
+            if constexpr (kExact) {  // the scores by their keys' factors, plus the logarithms of V's scales
+                const float4* kf = reinterpret_cast<const float4*>(smem + C::SC_OFF + (j & 1) * C::BN * 4);
+#pragma unroll
+                for (int i = 0; i < C::BN; i += 4) {
+                    const float4 a = kf[i / 4], b = kf[C::BN / 2 + i / 4];
+                    const float2 t0 = __ffma2_rn(make_float2(sv[i], sv[i + 1]), make_float2(a.x, a.y), make_float2(b.x, b.y));
+                    const float2 t1 = __ffma2_rn(make_float2(sv[i + 2], sv[i + 3]), make_float2(a.z, a.w), make_float2(b.z, b.w));
+                    sv[i] = t0.x, sv[i + 1] = t0.y, sv[i + 2] = t1.x, sv[i + 3] = t1.y;
+                }
+                __syncwarp();
+                if ((tid & 31) == 0) mbar_arrive(&f_free[2 * x + (j & 1)]);
+            }
             float mrow;
             if (all_vis) {
                 float r0 = sv[0], r1 = sv[1], r2 = sv[2], r3 = sv[3];
@@ -620,20 +715,39 @@ __global__ void __launch_bounds__(kPrefillInt8Threads, 1)
             const float smul = all_vis ? sl2 : 1.f;
             float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const float2 smul2 = make_float2(smul, smul), nm2 = make_float2(-mexp, -mexp);
+            if constexpr (kExact) ok = __all_sync(0xffffffffu, mbar_wait_or_abort(i_full, j & 1, abort_flag));
 #pragma unroll
             for (int c = 0; c < C::BN / 32; ++c) {
                 uint32_t pw[16];
+                if constexpr (kExact) {
+                    const float4* iv = reinterpret_cast<const float4*>(smem + C::IV_OFF + c * 128);
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const float2 arg = __ffma2_rn(make_float2(sv[c * 32 + i], sv[c * 32 + i + 1]), smul2, nm2);
-                    const float p0 = ex2_approx(arg.x), p1 = ex2_approx(arg.y);
-                    acc[(i / 2) & 1] = __fadd2_rn(acc[(i / 2) & 1], make_float2(p0, p1));
-                    pw[i / 2] = pack_half2(p0, p1);
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 r = iv[i / 4];
+                        const float2 u0 = __fadd2_rn(make_float2(sv[c * 32 + i], sv[c * 32 + i + 1]), nm2);
+                        const float2 u1 = __fadd2_rn(make_float2(sv[c * 32 + i + 2], sv[c * 32 + i + 3]), nm2);
+                        const float p0 = ex2_approx(u0.x), p1 = ex2_approx(u0.y), p2 = ex2_approx(u1.x), p3 = ex2_approx(u1.y);
+                        acc[0] = __ffma2_rn(make_float2(p0, p1), make_float2(r.x, r.y), acc[0]);
+                        acc[1] = __ffma2_rn(make_float2(p2, p3), make_float2(r.z, r.w), acc[1]);
+                        pw[i / 2] = pack_half2(p0, p1), pw[i / 2 + 1] = pack_half2(p2, p3);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 arg = __ffma2_rn(make_float2(sv[c * 32 + i], sv[c * 32 + i + 1]), smul2, nm2);
+                        const float p0 = ex2_approx(arg.x), p1 = ex2_approx(arg.y);
+                        acc[(i / 2) & 1] = __fadd2_rn(acc[(i / 2) & 1], make_float2(p0, p1));
+                        pw[i / 2] = pack_half2(p0, p1);
+                    }
                 }
                 tmem_st16_nowait(ts + c * 16, pw);
             }
             lsum = lsum * alpha + ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y));
-            alpha *= units.z;
+            if constexpr (kExact) {
+                __syncwarp();
+                if ((tid & 31) == 0) mbar_arrive(&i_free[x]);
+            }
+            alpha *= grown;
             if (j >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {

@@ -14,7 +14,8 @@ DT = {"f16": torch.float16, "bf16": torch.bfloat16}
 def reference(q, kp, vp, table, n, first, scale, dtype):
     """Attention in 64 bits of the rows q [r, Hq, D] over cached rows 0 .. first[i], and the error each element may have.
 
-    Keys and values go into the products as f16 numbers in units of their own: the unit puts the largest K row of a tile of 128
+    Fp16 queries take keys and values exactly, and are off by less than what follows for bf16 ones, whose keys and values go
+    into the products as f16 numbers in units of their own: the unit puts the largest K row of a tile of 128
     keys at 2^14 or above, the largest V row so far at 2^12 or above (an element is then below 2^15).  An element c S, |c| <= 1,
     is formed from S in two f16 parts: the split is off by 2^-22 of S, the second part's product by half a step (2^-22 of c S),
     the sum by half a step, 2^-11: 2^-11 + 2^-20 of the element, and 2^-25 for each of the three where f16 is subnormal, 3 *
@@ -218,3 +219,33 @@ def test_wide_tables_with_items_of_every_length(cols, Hkv):
     assert bool(torch.isnan(nan[140, 0]).all())
     nan[140, 0] = out[140, 0]
     assert torch.equal(nan, out)
+
+
+@pytest.mark.parametrize("D,G,B", [(128, 4, 32), (64, 2, 8), (128, 1, 16)])
+@pytest.mark.parametrize("ns,lens", [([9], [60]), ([140, 5], [400, 1500]), ([1, 2, 3], [1, 2, 3])])
+def test_fp16_queries_round_weights_and_results_alone(ns, lens, D, G, B):
+    """Large keys: a score off by 2^-11 of its terms would move the weights by more than the bound.  What is left with fp16
+    queries: a weight times its V row's scale to f16 (2^-11, or 2^-25 of the largest such product), the result's half step
+    (2^-11, or 2^-25), and fp32 scores: their sums, 2^-21 of the sum of the terms' magnitudes, the factor, the logarithm of
+    V's scale and the exponent, 4 roundings of 2^-24 of at most 2^9, and 2e-5 for the base-2 functions."""
+    kp, vp, bt = make_pools(lens, B, 2, D, seed=37, k_size=30.0)
+    q = torch.randn(sum(ns), 2 * G, D, device="cuda").half()
+    scale = D ** -0.5
+    out = prefill(q, kp, vp, bt, ns, lens, scale)
+    at = 0
+    for i, (n, L) in enumerate(zip(ns, lens)):
+        K, _ = rows_of(kp, bt[i], L)
+        V, vs = rows_of(vp, bt[i], L)
+        K, V, vs = (t.repeat_interleave(G, 1) for t in (K, V, vs))
+        qd = q[at: at + n].double()
+        t = torch.einsum("rhd,nhd->rhn", qd, K) * scale
+        t = t.masked_fill(torch.arange(L, device="cuda")[None, None, :] > torch.arange(L - n, L, device="cuda")[:, None, None],
+                          -float("inf"))
+        p = torch.softmax(t, -1)
+        ref, size = torch.einsum("rhn,nhd->rhd", p, V), torch.einsum("rhn,nhd->rhd", p, V.abs())
+        terms = scale * torch.einsum("rhd,nhd->rhn", qd.abs(), K.abs()).amax(-1)
+        ds = 2.0 ** -21 * terms + 4 * 2.0 ** -24 * 2.0 ** 9
+        bound = 2.0 ** -11 * ref.abs() * (1 + 2.0 ** -10) + (2.0 ** -11 + 2e-5 + 2 * ds)[..., None] * size \
+            + (L * 2.0 ** -25 * 127 * (p * vs.T[None]).amax(-1))[..., None] + 2.0 ** -25
+        check(out[at: at + n], ref, bound, f"chunk {i}")
+        at += n
