@@ -98,3 +98,56 @@ print('refused')
     env = dict(os.environ, PKV_CHECK="1", PYTHONPATH=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=200)
     assert r.returncode == 0 and "refused" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16], ids=["f16", "bf16"])
+def test_a_captured_step_replays_on_new_inputs(dt):
+    """Rotation and append, prefill of the chunks, a decode step and the rows read back, captured in one graph (the chunks of few
+    items take clusters), replayed on other inputs: the bits of the same calls one by one."""
+    B, Hq, H, D = 16, 8, 2, 128
+    ns, lens = [40, 3], [700, 130]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    kp, vp, bt = make_pools([n + 1 for n in lens], B, H, D, seed=3)
+    start = [kp.clone(), vp.clone()]
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    sl, qsl, cl = i32(*lens), i32(0, 40, 43), i32(*[n + 1 for n in lens])
+    pos = torch.cat([torch.arange(L - n, L, device="cuda") for n, L in zip(ns, lens)])
+    seq = torch.repeat_interleave(torch.arange(2, device="cuda"), torch.tensor(ns, device="cuda"))
+    slots = bt[seq, pos // B].long() * B + pos % B
+    last = torch.tensor(lens, device="cuda")
+    new_slots = bt[torch.arange(2, device="cuda"), last // B].long() * B + last % B
+    table = torch.empty(1024, 64, device="cuda")
+    pkv.rope_table(table)
+    q, k, v = (torch.zeros(43, h, D, dtype=dt, device="cuda") for h in (Hq, H, H))
+    q1, k1, v1 = (torch.zeros(2, h, D, dtype=dt, device="cuda") for h in (Hq, H, H))
+    qr, out, out1 = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q1)
+    rows = [torch.empty(43, H, D, device="cuda") for _ in range(2)]
+
+    def step():
+        pkv.rope_and_cache_int8(qr, q, k, v, table, pos, kp, vp, slots)
+        pkv.paged_attention_prefill_chunk_int8(out, qr, kp, vp, bt, sl, qsl, 40, 0.09)
+        pkv.paged_attention_decode_step_int8(k1, v1, new_slots, out1, q1, kp, vp, bt, cl, 0.09, max(lens) + 1,
+                                             total_context_tokens=sum(lens) + 2)
+        pkv.read_cache_int8(*rows, kp, vp, slots)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        for t in (q, k, v, q1, k1, v1):
+            t.copy_(torch.randn(t.shape, device="cuda", generator=g))
+        results = []
+        for call in (step, graph.replay):
+            kp.copy_(start[0])
+            vp.copy_(start[1])
+            for t in (qr, out, out1, *rows):
+                t.fill_(7.0)
+            call()
+            torch.cuda.synchronize()
+            results.append([t.clone() for t in (qr, out, out1, *rows, kp, vp)])
+        for a, b in zip(*results):
+            assert torch.equal(a, b)
+        assert bool(torch.isfinite(results[0][1]).all()) and bool(torch.isfinite(results[0][2]).all())
+    assert pkv.get_device_error() == 0

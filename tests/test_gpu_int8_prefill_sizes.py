@@ -122,6 +122,7 @@ def tiles_of_sizes(exponents, Hkv, D, which):
 def test_value_rows_that_grow_and_shrink_from_tile_to_tile(exponents, D, Hkv, ns_last):
     (kp, vp, bt), n = tiles_of_sizes(exponents, Hkv, D, "V")
     q = torch.randn(ns_last, Hkv, D, device="cuda").bfloat16()
+    compare(q.half(), kp, vp, bt, [ns_last], [n], D ** -0.5, f"tiles of {exponents}, fp16")
     compare(q, kp, vp, bt, [ns_last], [n], D ** -0.5, f"tiles of {exponents}")
 
 
@@ -129,7 +130,8 @@ def test_value_rows_that_grow_and_shrink_from_tile_to_tile(exponents, D, Hkv, ns
 @pytest.mark.parametrize("exponents", [(-3, 0, 3, -6, 2), (-40, -20, 0, None), (None, None)], ids=str)
 def test_key_rows_that_grow_and_shrink_from_tile_to_tile(exponents, Hkv, ns_last):
     (kp, vp, bt), n = tiles_of_sizes(exponents, Hkv, 128, "K")
-    q = torch.randn(ns_last, Hkv, 128, device="cuda").half()
+    q = torch.randn(ns_last, Hkv, 128, device="cuda").bfloat16()
+    compare(q.half(), kp, vp, bt, [ns_last], [n], 0.04, f"tiles of {exponents}, fp16")
     compare(q, kp, vp, bt, [ns_last], [n], 0.04, f"tiles of {exponents}")
 
 
@@ -249,3 +251,20 @@ def test_fp16_queries_round_weights_and_results_alone(ns, lens, D, G, B):
             + (L * 2.0 ** -25 * 127 * (p * vs.T[None]).amax(-1))[..., None] + 2.0 ** -25
         check(out[at: at + n], ref, bound, f"chunk {i}")
         at += n
+
+
+def test_fp16_queries_take_rows_of_any_finite_size():
+    """Rows beyond fp16's largest value, in K and in V, under fp16 queries: the scores' scale undoes K's size, and a V row of
+    1e6 weighs little enough (or shows as an infinity, as the decode's result does)."""
+    ns, lens = [20], [90]
+    kp, vp, bt = make_pools(lens, 16, 2, 128, seed=41, k_size=1e7)
+    q = torch.randn(20, 4, 128, device="cuda").half()
+    compare(q, kp, vp, bt, ns, lens, 9e-9, "K rows of 1e7")
+    kp, vp, bt = make_pools(lens, 16, 2, 128, seed=43, v_size=1e6)
+    out = prefill(q, kp, vp, bt, ns, lens, 0.09)
+    dec = torch.empty_like(q[:1])
+    pkv.paged_attention_decode_int8(dec, q[-1:], kp, vp, bt, torch.tensor([90], dtype=torch.int32, device="cuda"), 0.09, 90)
+    assert bool(torch.isinf(out).any()) and not bool(torch.isnan(out).any())
+    far = dec.abs() > 60000
+    assert torch.equal(torch.isinf(out[-1]) | far[0], far[0])
+    assert bool(((out[-1] - dec[0]).abs()[~far[0]] <= 2.0 ** -6 * 65504).all())
